@@ -262,7 +262,7 @@ def run(st):
         if case["op"] == "append":
             turn = {"q": st["q"], "freqs": st["freqs"], "sections": st["sections"], "positions": st["positions"]}
             q = hstu.hstu_paged_append(st["k"], st["v"], st["k_cache"], st["v_cache"], st["table"], st["q_offsets"],
-                                       st["kv_len"], st["max_new"], **(turn if case["rotate"] else {}))
+                                       st["kv_len"], **(turn if case["rotate"] else {}))
             return q, st["k_cache"], st["v_cache"]
         return hstu.hstu_paged_attn_fwd(st["q"], st["k_cache"], st["v_cache"], st["table"], st["q_offsets"],
                                         st["kv_len"], st["num_targets"], st["alpha"], st["N"], st["max_new"], st["max_kv"])
