@@ -5,7 +5,8 @@
 over jagged batches of user-interaction histories with appended candidate tokens (history
 causal, each candidate sees all history plus itself), plus the streaming variant that queries
 only new tokens against a cached K/V prefix.  The work happens in ``libhstu_attn.so`` (C ABI in
-``include/hstu_attn.h``); :mod:`.binding` marshals torch tensors into it.  The binding's names
+``include/hstu_attn.h``); :mod:`.binding` marshals torch tensors into it, and :mod:`.paged` does so for the
+paged K/V cache and the position rotation (``include/hstu_paged.h``).  Their names
 are re-exported lazily so that :mod:`.workloads` and :mod:`.metrics` import without it.
 """
 _BINDING_NAMES = ("HstuError", "hstu_attn_fwd", "hstu_attn_fwd_cached", "hstu_attn_fwd_rab", "hstu_attn_plan_bytes", "hstu_attn_plan",
@@ -14,9 +15,14 @@ _BINDING_NAMES = ("HstuError", "hstu_attn_fwd", "hstu_attn_fwd_cached", "hstu_at
                   "hstu_layer_fwd", "hstu_layers_fwd", "plan_contents",
                   "library_path", "load_library")
 
+_PAGED_NAMES = ("hstu_rotary", "hstu_rotary_freqs", "hstu_paged_append", "hstu_paged_attn_fwd")
+
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
         return getattr(binding, name)
+    if name in _PAGED_NAMES:
+        from . import paged
+        return getattr(paged, name)
     raise AttributeError(name)

@@ -1,4 +1,4 @@
-"""Builds ``libhstu_attn.so`` (the CUDA library behind include/hstu_attn.h) in-tree for sm_100a."""
+"""Builds ``libhstu_attn.so`` (the CUDA library behind include/hstu_attn.h and include/hstu_paged.h) in-tree for sm_100a."""
 import os
 import subprocess
 import sys
@@ -8,15 +8,15 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhstu_attn.so")
-SOURCES = ["hstu_attn.cu"]
+SOURCES = ["hstu_attn.cu", "hstu_paged.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-         "-Xcompiler", "-fPIC", "-shared", "-I" + INCLUDE, "-I" + CSRC]
+         "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I" + INCLUDE, "-I" + CSRC]
 
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "hstu_attn.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -17,6 +17,7 @@
 #include <mutex>
 #include <vector>
 
+#include "host_state.h"
 #include "hstu_attn.h"
 #include "hstu_bwd_dq_sm100.cuh"
 #include "hstu_bwd_sm100.cuh"
@@ -33,14 +34,6 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
-  std::once_flag once;
-  cudaError_t init_err = cudaSuccess;
-  int num_sms = 0;
-  int gemm_clusters = 0;  // resident two-CTA clusters of the two-SM GEMM
-  cudaMemPool_t pool = nullptr;
-  unsigned* err_word = nullptr;
-};
 DeviceState g_dev[kMaxDevices];
 
 std::once_flag g_encode_once;
@@ -110,14 +103,6 @@ void init_device(DeviceState& st, int dev) {
   st.init_err = e;
 }
 
-DeviceState* device_state() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-  DeviceState& st = g_dev[dev];
-  std::call_once(st.once, init_device, std::ref(st), dev);
-  return st.init_err == cudaSuccess ? &st : nullptr;
-}
-
 bool encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
@@ -153,13 +138,6 @@ bool encode_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t col
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
 }
 
 // Plan layout (documented in include/hstu_attn.h):
@@ -709,6 +687,16 @@ hstu_status_t run_bwd(const void* q, const void* k, const void* v, const void* d
 }
 
 }  // namespace
+
+DeviceState* device_state() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  DeviceState& st = g_dev[dev];
+  std::call_once(st.once, init_device, std::ref(st), dev);
+  return st.init_err == cudaSuccess ? &st : nullptr;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encoder() ? g_encode : nullptr; }
 
 // ---------------------------------------------------------------------------------------------
 // Allocation-free variant (hstu_attn_fwd_noalloc).  Its plan lives in this fixed device array

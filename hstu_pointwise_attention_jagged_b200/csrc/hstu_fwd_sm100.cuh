@@ -161,7 +161,7 @@ __device__ __forceinline__ uint32_t suspend_hint(uint64_t limit_ns) {
 // Slow path of wait_bounded: waits until the phase completes, the CTA aborts, or the time limit.
 // Each try_wait may itself suspend the thread for a while, so the flag and the clock are checked
 // after every attempt.
-__device__ __noinline__ bool wait_bounded_slow(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag,
+static __device__ __noinline__ bool wait_bounded_slow(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag,
                                                unsigned* err, uint64_t limit_ns) {
   const uint64_t t0 = ptx::globaltimer_ns();
   const bool poll = limit_ns < kPollBelowNs;
@@ -188,7 +188,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
 }
 
 // Abort-path drain: waits for phase `parity` of `bar` for at most kDrainLimitNs.
-__device__ __noinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+static __device__ __noinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (!ptx::mbar_try_wait_for(bar, parity, (uint32_t)kDrainLimitNs))
     if (ptx::globaltimer_ns() - t0 > kDrainLimitNs) return;
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
 // attention kernel uses, on an mbarrier that nothing ever arrives on.  After limit_ns the wait
 // gives up, records kErrTimeout in the error word and raises the abort flag, and the kernel
 // returns normally: no trap, no hang, and the context stays usable.
-__global__ void wait_timeout_selfcheck_kernel(unsigned* err, uint64_t limit_ns) {
+static __global__ void wait_timeout_selfcheck_kernel(unsigned* err, uint64_t limit_ns) {
   __shared__ uint64_t never;
   __shared__ int32_t abort_flag;
   if (threadIdx.x == 0) {

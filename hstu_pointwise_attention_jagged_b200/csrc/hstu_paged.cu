@@ -1,0 +1,223 @@
+// hstu_paged.cu — host side of the calls declared in include/hstu_paged.h: argument checks, launch
+// shapes and tensor maps.  Nothing synchronises; nothing falls back to another path.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "host_state.h"
+#include "hstu_paged.h"
+#include "paged_cache.cuh"
+#include "rotary_sm100.cuh"
+
+namespace hstu {
+namespace {
+
+bool head_size_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
+
+// A token tensor's row stride: at least the packed row, a multiple of 16 bytes.
+hstu_status_t check_ld(int64_t ld, int64_t width) {
+  if (ld < width) return HSTU_ERR_INVALID_ARGUMENT;
+  return (ld % 8) == 0 ? HSTU_OK : HSTU_ERR_UNSUPPORTED;
+}
+
+// Whether two row blocks of `width` elements share an element.  Blocks of one wide matrix (equal
+// strides) interleave without touching: their columns are compared.
+bool rows_overlap(const void* a, int64_t a_ld, const void* b, int64_t b_ld, int64_t rows, int64_t width) {
+  if (!overlaps(a, static_cast<size_t>((rows - 1) * a_ld + width) * 2, b,
+                static_cast<size_t>((rows - 1) * b_ld + width) * 2))
+    return false;
+  if (a_ld != b_ld) return true;
+  int64_t off = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 2 % a_ld;
+  if (off < 0) off += a_ld;
+  return off < width || a_ld - off < width;
+}
+
+// An output that is its own input (same rows, same stride) is written by the thread that read it.
+bool clashes(const void* out, int64_t out_ld, const void* in, int64_t in_ld, bool own, int64_t rows, int64_t width) {
+  if (own && out == in && out_ld == in_ld) return false;
+  return rows_overlap(out, out_ld, in, in_ld, rows, width);
+}
+
+hstu_status_t check_rotation(const hstu_rotation_t* r, int32_t d, int64_t rows, bool need_positions) {
+  if (!r || r->pairs < 1 || r->axes < 1 || r->axes > HSTU_MAX_AXES) return HSTU_ERR_INVALID_ARGUMENT;
+  if (2 * static_cast<int64_t>(r->pairs) > d) return HSTU_ERR_INVALID_ARGUMENT;
+  int64_t sum = 0;
+  for (int a = 0; a < r->axes; ++a) {
+    if (r->sections[a] < 0) return HSTU_ERR_INVALID_ARGUMENT;
+    sum += r->sections[a];
+  }
+  if (sum != r->pairs) return HSTU_ERR_INVALID_ARGUMENT;
+  if (r->pairs % 8 != 0) return HSTU_ERR_UNSUPPORTED;
+  if (rows == 0) return HSTU_OK;
+  if (!r->freqs || (!r->positions && (need_positions || r->axes > 1))) return HSTU_ERR_INVALID_ARGUMENT;
+  if (r->positions && r->axes > 1 && r->positions_ld < rows) return HSTU_ERR_INVALID_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(r->freqs) & 7u) || (reinterpret_cast<uintptr_t>(r->positions) & 3u))
+    return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+
+hstu_status_t check_cache(const hstu_paged_cache_t* c, int32_t H, int32_t d) {
+  if (!c || !c->k || !c->v || c->num_pages < 1 || c->table_width < 0 || c->table_ld < c->table_width)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (c->table_width > 0 && !c->page_table) return HSTU_ERR_INVALID_ARGUMENT;
+  if (c->page_size < 8 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return HSTU_ERR_UNSUPPORTED;
+  const int64_t strides[3] = {c->page_stride, c->row_stride, c->head_stride};
+  for (int64_t s : strides) {
+    if (s < d) return HSTU_ERR_INVALID_ARGUMENT;
+    if (s % 8 != 0 || s > (1ll << 38)) return HSTU_ERR_UNSUPPORTED;  // tensor-map strides are < 2^40 bytes
+  }
+  if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u))
+    return HSTU_ERR_UNSUPPORTED;
+  (void)H;
+  return HSTU_OK;
+}
+
+// Bytes from the first to past the last element of K (and of V).
+size_t cache_bytes(const hstu_paged_cache_t& c, int32_t H, int32_t d) {
+  return static_cast<size_t>((c.num_pages - 1) * c.page_stride + (c.page_size - 1) * c.row_stride +
+                             static_cast<int64_t>(H - 1) * c.head_stride + d) * 2;
+}
+
+PagedView view_of(const hstu_paged_cache_t& c) {
+  PagedView v;
+  v.k = static_cast<__nv_bfloat16*>(c.k);
+  v.v = static_cast<__nv_bfloat16*>(c.v);
+  v.page_stride = c.page_stride;
+  v.row_stride = c.row_stride;
+  v.head_stride = c.head_stride;
+  v.num_pages = c.num_pages;
+  v.page_shift = __builtin_ctz(static_cast<unsigned>(c.page_size));
+  v.table = c.page_table;
+  v.table_width = c.table_width;
+  v.table_ld = c.table_ld;
+  return v;
+}
+
+void add_tensor(RotArgs& a, const void* src, int64_t ld, void* dst, int64_t dst_ld, RotTarget target, bool rotated) {
+  RotTensor& t = a.t[a.tensors++];
+  t.src = static_cast<const __nv_bfloat16*>(src);
+  t.src_ld = ld;
+  t.dst = static_cast<__nv_bfloat16*>(dst);
+  t.dst_ld = dst_ld;
+  t.target = target;
+  t.rotated = rotated;
+}
+
+void set_rotation(RotArgs& a, const hstu_rotation_t* r, bool inverse) {
+  if (!r) return;
+  a.freqs = r->freqs;
+  a.positions = r->positions;
+  a.positions_ld = r->positions_ld;
+  a.pairs = r->pairs;
+  a.axes = r->axes;
+  int32_t end = 0;
+  for (int i = 0; i + 1 < r->axes; ++i) a.section_end[i] = end += r->sections[i];
+  a.interleaved = r->interleaved != 0;
+  a.sign = inverse ? -1.0f : 1.0f;
+}
+
+// Rows of a block: about four batches' worth of units for its threads, fewer where that would leave
+// SMs without a block (a call for a few rows is bound by the latency of one block).
+hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState& st, cudaStream_t stream) {
+  a.head_shift = d == 128 ? 3 : (d == 64 ? 2 : 1);
+  const int64_t row_units = static_cast<int64_t>(a.tensors) * a.H << a.head_shift;
+  int64_t r = kRotThreads * kRotBatch / row_units;
+  const int64_t spread = a.rows / (2 * st.num_sms);
+  r = r < spread ? r : spread;
+  a.rows_per_block = static_cast<int32_t>(r < 1 ? 1 : (r > kRotMaxRows ? kRotMaxRows : r));
+  const int grid = (a.rows + a.rows_per_block - 1) / a.rows_per_block;
+  if (paged) rotary_kernel<true><<<grid, kRotThreads, 0, stream>>>(a);
+  else rotary_kernel<false><<<grid, kRotThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace hstu
+
+extern "C" {
+
+hstu_status_t hstu_rotary(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const hstu_rotation_t* rotation,
+                          int32_t inverse, int32_t H, int32_t d, int32_t rows, void* q_out, int64_t q_out_ld,
+                          void* k_out, int64_t k_out_ld, void* stream) {
+  using namespace hstu;
+  if (H < 1 || rows < 0 || (inverse != 0 && inverse != 1)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4) return HSTU_ERR_UNSUPPORTED;
+  hstu_status_t s = check_rotation(rotation, d, rows, true);
+  if (s != HSTU_OK || rows == 0) return s;
+  if (!q || !q_out || (k == nullptr) != (k_out == nullptr)) return HSTU_ERR_INVALID_ARGUMENT;
+  const int64_t width = static_cast<int64_t>(H) * d;
+  const int64_t lds[4] = {q_ld, q_out_ld, k ? k_ld : width, k ? k_out_ld : width};
+  for (int64_t ld : lds)
+    if ((s = check_ld(ld, width)) != HSTU_OK) return s;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return HSTU_ERR_UNSUPPORTED;
+  if (clashes(q_out, q_out_ld, q, q_ld, true, rows, width)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (k && (clashes(k_out, k_out_ld, k, k_ld, true, rows, width) ||
+            clashes(q_out, q_out_ld, k, k_ld, false, rows, width) ||
+            clashes(k_out, k_out_ld, q, q_ld, false, rows, width) ||
+            clashes(k_out, k_out_ld, q_out, q_out_ld, false, rows, width)))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  DeviceState* st = device_state();
+  if (!st) return HSTU_ERR_CUDA;
+  RotArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.rows = rows;
+  a.H = H;
+  add_tensor(a, q, q_ld, q_out, q_out_ld, kToRows, true);
+  if (k) add_tensor(a, k, k_ld, k_out, k_out_ld, kToRows, true);
+  set_rotation(a, rotation, inverse != 0);
+  return launch_rotary(a, d, false, *st, static_cast<cudaStream_t>(stream));
+}
+
+hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                                const hstu_rotation_t* rotation, const hstu_paged_cache_t* cache,
+                                const int32_t* q_offsets, const int32_t* kv_len, int32_t B, int32_t H, int32_t d,
+                                int32_t total_new, void* q_out, int64_t q_out_ld, void* stream) {
+  using namespace hstu;
+  if (B < 0 || H < 1 || total_new < 0) return HSTU_ERR_INVALID_ARGUMENT;
+  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4) return HSTU_ERR_UNSUPPORTED;
+  hstu_status_t s = check_cache(cache, H, d);
+  if (s == HSTU_OK && rotation) s = check_rotation(rotation, d, total_new, false);
+  if (s != HSTU_OK || total_new == 0 || B == 0) return s;
+  if (!k || !v || !q_offsets || !kv_len) return HSTU_ERR_INVALID_ARGUMENT;
+  if ((q == nullptr) != (q_out == nullptr) || (q && !rotation)) return HSTU_ERR_INVALID_ARGUMENT;
+  const int64_t width = static_cast<int64_t>(H) * d;
+  const int64_t lds[4] = {k_ld, v_ld, q ? q_ld : width, q ? q_out_ld : width};
+  for (int64_t ld : lds)
+    if ((s = check_ld(ld, width)) != HSTU_OK) return s;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return HSTU_ERR_UNSUPPORTED;
+  // The cache overlaps no token tensor; K and V pages may interleave, so only identical ones are refused.
+  const size_t pool = cache_bytes(*cache, H, d);
+  const void* tokens[4] = {k, v, q, q_out};
+  for (int i = 0; i < (q ? 4 : 2); ++i) {
+    const size_t n = static_cast<size_t>((total_new - 1) * lds[i] + width) * 2;
+    if (overlaps(cache->k, pool, tokens[i], n) || overlaps(cache->v, pool, tokens[i], n))
+      return HSTU_ERR_INVALID_ARGUMENT;
+  }
+  if (cache->k == cache->v) return HSTU_ERR_INVALID_ARGUMENT;
+  if (q && (clashes(q_out, q_out_ld, q, q_ld, true, total_new, width) ||
+            clashes(q_out, q_out_ld, k, k_ld, false, total_new, width) ||
+            clashes(q_out, q_out_ld, v, v_ld, false, total_new, width)))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  DeviceState* st = device_state();
+  if (!st) return HSTU_ERR_CUDA;
+  RotArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.rows = total_new;
+  a.H = H;
+  if (q) add_tensor(a, q, q_ld, q_out, q_out_ld, kToRows, true);
+  add_tensor(a, k, k_ld, nullptr, 0, kToCacheK, rotation != nullptr);
+  add_tensor(a, v, v_ld, nullptr, 0, kToCacheV, false);
+  set_rotation(a, rotation, false);
+  a.cache = view_of(*cache);
+  a.q_offsets = q_offsets;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.err = st->err_word;
+  return launch_rotary(a, d, true, *st, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

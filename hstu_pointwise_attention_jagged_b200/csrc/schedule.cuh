@@ -175,7 +175,7 @@ __device__ __forceinline__ int owner_of(const int32_t* block_start, int B, int g
 // L2, instead of every user's tiles being fetched again for each cost level.  A batch whose K and
 // V fit the window is one wave, ordered by cost alone.  The per-block passes run one thread per
 // (user, 128-row block).
-__global__ void __launch_bounds__(kSchedThreads) schedule_kernel(const SchedArgs a) {
+static __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(const SchedArgs a) {
   // A dependent attention kernel may start its prologue now; it waits for this grid's writes
   // (griddepcontrol.wait) before it reads anything in global memory.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

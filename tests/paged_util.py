@@ -1,0 +1,94 @@
+"""Helpers of the paged-cache and rotation tests: a plain fp64 rotation, random page pools, and the
+jagged K/V that a page pool holds."""
+import numpy as np
+import torch
+
+from gpu_util import dev_i32
+
+
+def rotate64(x, positions, freqs, sections, interleaved=False, inverse=False):
+    """x: [rows, H, d] float64; positions: [axes, rows]; the formula of include/hstu_paged.h, pair by pair."""
+    x = np.asarray(x, np.float64)
+    y = x.copy()
+    n = len(freqs)
+    axis = [a for a, k in enumerate(sections) for _ in range(k)]
+    for i in range(n):
+        # Long double: a 31-bit position times a frequency carries 2^-53 of its size in fp64.
+        t = positions[axis[i]].astype(np.longdouble) * np.longdouble(freqs[i])
+        c, s = np.cos(t).astype(np.float64)[:, None], np.sin(t).astype(np.float64)[:, None]
+        if inverse:
+            s = -s
+        lo, hi = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+        y[..., lo] = x[..., lo] * c - x[..., hi] * s
+        y[..., hi] = x[..., lo] * s + x[..., hi] * c
+    return y
+
+
+def rotation_bound(x, want, pairs, interleaved):
+    """Largest error a correct rotation makes, element by element.  The value is rounded to bf16 once
+    (half a step: 2^-8 of it).  Before that, times the pair's |x| + |y|: the angle in fp64 turns is off by
+    three roundings of 2^-53 of at most 2^28.4 turns (positions below 2^31, frequencies up to 1),
+    7.8e-7 radians; its fraction rounded to fp32 by 2^-25 turns, 1.9e-7; sincospif by two steps, 1.2e-7;
+    and three fp32 operations by 2^-24 each, 1.8e-7: 1.3e-6 < 2^-19.5 in all."""
+    x = np.abs(np.asarray(x, np.float64))
+    s = np.zeros_like(x)
+    for i in range(pairs):
+        lo, hi = (2 * i, 2 * i + 1) if interleaved else (i, i + pairs)
+        s[..., lo] = s[..., hi] = x[..., lo] + x[..., hi]
+    pre = s * 2.0 ** -19.5
+    return pre + (np.abs(want) + pre) * 2.0 ** -8 + 1e-38
+
+
+def bf16_normal(gen, *shape):
+    return torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+
+class Pool:
+    """A page pool with every user's pages in random places; unused table entries are -1 or garbage.
+
+    layout: "rows" [pages, P, H, d], "heads" [pages, H, P, d], "halves" K and V as the two halves of
+    [pages, 2, P, H, d]."""
+
+    def __init__(self, lengths, page, H, d, layout="rows", seed=0, spare=3, fill=float("nan"), extra_width=2):
+        rng = np.random.default_rng(seed)
+        self.lengths = np.asarray(lengths, np.int64)
+        self.page, self.H, self.d = page, H, d
+        need = -(-self.lengths // page)
+        self.pages = int(need.sum()) + spare
+        order = rng.permutation(self.pages)
+        width = int(need.max(initial=0)) + extra_width
+        table = rng.integers(-5, 1 << 30, size=(len(lengths), width)).astype(np.int32)  # garbage where unused
+        at = 0
+        for b, n in enumerate(need):
+            table[b, :n] = order[at:at + n]
+            at += int(n)
+        self.table_h = table
+        self.table = dev_i32(table).view(table.shape)
+        if layout == "rows":
+            self.k, self.v = (torch.full((self.pages, page, H, d), fill, dtype=torch.bfloat16, device="cuda")
+                              for _ in range(2))
+        elif layout == "heads":
+            self.k, self.v = (torch.full((self.pages, H, page, d), fill, dtype=torch.bfloat16, device="cuda")
+                              .transpose(1, 2) for _ in range(2))
+        else:
+            both = torch.full((self.pages, 2, page, H, d), fill, dtype=torch.bfloat16, device="cuda")
+            self.k, self.v = both[:, 0], both[:, 1]
+
+    def where(self, b, lo, hi):
+        """(page, row) index tensors of user b's positions [lo, hi)."""
+        j = np.arange(lo, hi)
+        pages = self.table_h[b, j // self.page].astype(np.int64)
+        return torch.from_numpy(pages).cuda(), torch.from_numpy(j % self.page).cuda()
+
+    def put(self, b, lo, k, v):
+        at = self.where(b, lo, lo + k.shape[0])
+        self.k[at] = k
+        self.v[at] = v
+
+    def rows(self, b, lo, hi):
+        at = self.where(b, lo, hi)
+        return self.k[at], self.v[at]
+
+
+def offsets_of(counts):
+    return dev_i32(np.concatenate([[0], np.cumsum(counts)]))
