@@ -7,10 +7,12 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "host_state.h"
 #include "hstu_paged.h"
 #include "paged_cache.cuh"
+#include "paged_rows_sm100.cuh"
 #include "rotary_sm100.cuh"
 
 namespace hstu {
@@ -135,6 +137,47 @@ hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState
   return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
+// CTAs that share one (user, head, row block) in the few-rows kernel.
+int rows_split(int64_t clusters, int64_t tiles, int num_sms) {
+  int s = 1;
+  while (s < kRowsMaxSplit && clusters * s < 4 * static_cast<int64_t>(num_sms) && s < tiles) s *= 2;
+  return s;
+}
+
+template <int D>
+hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t stream) {
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return HSTU_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  std::call_once(once[dev], [&] {
+    e = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::kSmemBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (e != cudaSuccess) return HSTU_ERR_CUDA;
+  const int64_t clusters = static_cast<int64_t>(a.B) * a.H * a.blocks;
+  const int64_t tiles = (a.max_kv + RowsCfg<D>::kKeys - 1) / RowsCfg<D>::kKeys;
+  int S = rows_split(clusters, tiles, st.num_sms);
+  if (clusters * S > INT_MAX) return HSTU_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * S));
+  cfg.blockDim = dim3(kRowsThreads);
+  cfg.dynamicSmemBytes = RowsCfg<D>::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D>, a) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace hstu
 
@@ -218,6 +261,50 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
   a.B = B;
   a.err = st->err_word;
   return launch_rotary(a, d, true, *st, static_cast<cudaStream_t>(stream));
+}
+
+hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_cache_t* cache, const int32_t* q_offsets,
+                                  const int32_t* kv_len, const int32_t* num_targets, int32_t B, int32_t H, int32_t d,
+                                  int32_t total_new, int32_t max_new, int32_t max_kv, float alpha, float N, void* out,
+                                  int64_t out_ld, void* stream) {
+  using namespace hstu;
+  if (B < 0 || H < 1 || total_new < 0 || max_new < 0 || max_kv < 0) return HSTU_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(alpha) || !std::isfinite(N) || !(N > 0.0f)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4 || max_kv > INT_MAX - 4096)
+    return HSTU_ERR_UNSUPPORTED;
+  hstu_status_t s = check_cache(cache, H, d);
+  if (s != HSTU_OK || total_new == 0 || B == 0) return s;
+  if (!q || !q_offsets || !kv_len || !out) return HSTU_ERR_INVALID_ARGUMENT;
+  const int64_t width = static_cast<int64_t>(H) * d;
+  if ((s = check_ld(q_ld, width)) != HSTU_OK || (s = check_ld(out_ld, width)) != HSTU_OK) return s;
+  if (!aligned16(q) || !aligned16(out)) return HSTU_ERR_UNSUPPORTED;
+  const size_t pool = cache_bytes(*cache, H, d), out_bytes = static_cast<size_t>((total_new - 1) * out_ld + width) * 2;
+  if (overlaps(cache->k, pool, out, out_bytes) || overlaps(cache->v, pool, out, out_bytes) ||
+      rows_overlap(out, out_ld, q, q_ld, total_new, width))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  DeviceState* st = device_state();
+  if (!st) return HSTU_ERR_CUDA;
+  RowsArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_ld = q_ld;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.out_ld = out_ld;
+  a.cache = view_of(*cache);
+  a.q_offsets = q_offsets;
+  a.kv_len = kv_len;
+  a.num_targets = num_targets;
+  a.B = B;
+  a.H = H;
+  const int32_t most = max_new < total_new ? max_new : total_new;
+  a.blocks = most > kRowsBlock ? (most + kRowsBlock - 1) / kRowsBlock : 1;
+  a.total_new = total_new;
+  a.max_new = max_new;
+  a.max_kv = max_kv;
+  a.half_alpha = 0.5f * alpha;
+  a.inv_n = 1.0f / N;
+  a.err = st->err_word;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_rows<128>(a, *st, cs) : (d == 64 ? launch_rows<64>(a, *st, cs) : launch_rows<32>(a, *st, cs));
 }
 
 }  // extern "C"

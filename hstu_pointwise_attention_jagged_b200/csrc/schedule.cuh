@@ -26,17 +26,19 @@ struct TileRange {
   int e1, s2, e2;
 };
 
+// kKeys: keys of a tile.
+template <int kKeys = kTileRows>
 __host__ __device__ __forceinline__ TileRange key_tiles(int p0, int p1, int U) {
   TileRange r{0, 0, 0};
   if (p1 <= p0) return r;
   if (p1 <= U) {
-    r.e1 = cdiv(p1, kTileRows);
+    r.e1 = cdiv(p1, kKeys);
     r.s2 = r.e2 = r.e1;
     return r;
   }
-  r.e1 = cdiv(U, kTileRows);
-  const int s = (p0 > U ? p0 : U) / kTileRows;
-  const int e = cdiv(p1, kTileRows);
+  r.e1 = cdiv(U, kKeys);
+  const int s = (p0 > U ? p0 : U) / kKeys;
+  const int e = cdiv(p1, kKeys);
   if (s <= r.e1) {
     r.e1 = (e > r.e1) ? e : r.e1;
     r.s2 = r.e2 = r.e1;

@@ -17,6 +17,7 @@ MAX_AXES = 4
 EXPORTS = (
     "hstu_rotary",
     "hstu_paged_append",
+    "hstu_paged_attn_fwd",
 )
 
 
@@ -47,6 +48,8 @@ def load_library():
         rot, cache = ctypes.POINTER(Rotation), ctypes.POINTER(PagedCache)
         lib.hstu_rotary.argtypes = [vp, i64, vp, i64, rot, i32, i32, i32, i32, vp, i64, vp, i64, vp]
         lib.hstu_paged_append.argtypes = [vp, i64, vp, i64, vp, i64, rot, cache, vp, vp, i32, i32, i32, i32, vp, i64, vp]
+        f32 = ctypes.c_float
+        lib.hstu_paged_attn_fwd.argtypes = [vp, i64, cache, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, i64, vp]
         for name in EXPORTS:
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
@@ -189,3 +192,29 @@ def hstu_paged_append(k, v, k_cache, v_cache, page_table, q_offsets, kv_len, q=N
                                    _ptr(kv_len), B, H, d, total, _ptr(q_out), qo_ld, _stream_ptr(stream, dev))
     _raise_if(st, "hstu_paged_append")
     return q_out
+
+
+def hstu_paged_attn_fwd(q, k_cache, v_cache, page_table, q_offsets, kv_len, num_targets, alpha, N, max_new, max_kv,
+                        out=None, stream=None):
+    """Attention of each user's new rows q (bf16 [total_new, H, d], packed by q_offsets) over its kv_len rows
+    in the paged cache, the new ones included; the last num_targets of them are candidates.  Returns
+    ``out``.  See include/hstu_paged.h."""
+    lib = load_library()
+    q_ld = _check_rows("q", q)
+    total, H, d = q.shape
+    dev = q.device
+    B = q_offsets.numel() - 1
+    _check_index("q_offsets", q_offsets, B + 1, dev, optional=False)
+    _check_index("kv_len", kv_len, B, dev, optional=False)
+    _check_index("num_targets", num_targets, B, dev)
+    cache = _cache(k_cache, v_cache, page_table, B, dev)
+    if k_cache.shape[2:] != q.shape[1:]:
+        raise ValueError("the cache holds [%d, %d] rows, q has [%d, %d]" % (*k_cache.shape[2:], H, d))
+    out = torch.empty((total, H, d), dtype=q.dtype, device=dev) if out is None else out
+    out_ld = _check_rows("out", out, H, d, total, dev)
+    with torch.cuda.device(dev):
+        st = lib.hstu_paged_attn_fwd(_ptr(q), q_ld, ctypes.byref(cache), _ptr(q_offsets), _ptr(kv_len), _ptr(num_targets),
+                                     B, H, d, total, int(max_new), int(max_kv), float(alpha), float(N), _ptr(out), out_ld,
+                                     _stream_ptr(stream, dev))
+    _raise_if(st, "hstu_paged_attn_fwd")
+    return out

@@ -123,6 +123,36 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
                                 int32_t B, int32_t H, int32_t d, int32_t total_new,
                                 void* q_out, int64_t q_out_ld, void* stream);
 
+/*
+ * hstu_paged_attn_fwd — hstu_attn_fwd_cached over the paged cache: each user's new rows attend to its
+ * kv_len[b] cached rows, which include the new ones (hstu_paged_append has written them).
+ *
+ *     out[i,h,:] = (1/N) * sum_{j in A(i)} silu(alpha * <q[i,h,:], k[j,h,:]>) * v[j,h,:]
+ *
+ * with A(i) as in hstu_attn.h: the last num_targets[b] of the new rows are candidates, which see the
+ * history and themselves; the others are history and see what precedes them and themselves.  A row
+ * always sees itself, so no row is empty.
+ *   q             device bf16 [total_new, H, d], rows q_ld elements apart; d in {32, 64, 128}.
+ *   cache         see above; read only.
+ *   q_offsets, kv_len   as in hstu_paged_append.
+ *   num_targets   device int32 [B], 0 <= T_b <= n_b; NULL means none.
+ *   max_new, max_kv     upper bounds on every n_b and kv_len[b] (they choose the kernel and its launch
+ *                 shape; a user beyond them is reported as HSTU_ERR_BAD_OFFSETS and skipped).
+ *   alpha, N      as in hstu_attn_fwd.
+ *   out           device bf16 [total_new, H, d], rows out_ld apart; may overlap neither q nor the cache.
+ * K, V and q must be finite in the rows that a user owns: a tile's masked pairs get the weight zero, but
+ * zero times an infinite V of the same user is not zero.  Nothing else in the cache needs to be:
+ * rows behind a user's last one may hold anything.
+ * Errors on the host as in hstu_paged_append.  On the device, HSTU_ERR_BAD_OFFSETS for inconsistent
+ * offsets or lengths (the user's rows of out are not written) and for a table entry outside the pool
+ * (its rows count as zeros).
+ */
+hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_cache_t* cache,
+                                  const int32_t* q_offsets, const int32_t* kv_len,
+                                  const int32_t* num_targets, int32_t B, int32_t H, int32_t d,
+                                  int32_t total_new, int32_t max_new, int32_t max_kv,
+                                  float alpha, float N, void* out, int64_t out_ld, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -92,3 +92,28 @@ class Pool:
 
 def offsets_of(counts):
     return dev_i32(np.concatenate([[0], np.cumsum(counts)]))
+
+
+def dense64(q, k, v, c, n, T, alpha, N):
+    """One user in fp64: q [n, H, d] at positions c .. c + n, k and v [c + n, H, d], the last T rows
+    candidates.  Returns the outputs and a bound on a correct kernel's error, element by element.
+
+    The bound: p = silu(x) is rounded to bf16 for its product with v (half a step, 2^-8 of p); it is
+    formed as h + h tanh(h), h = x / 2, with a tanh good to 2^-10.9 (PTX tanh.approx.f32), which moves
+    p by at most 2^-10.9 |h|; scores are fp32 sums of d products (d 2^-24 of the sum of their sizes,
+    and |silu'| < 1.1), outputs fp32 sums of L terms (L 2^-24 of the sum of their sizes); the output
+    is rounded once (2^-8 of it)."""
+    L, U = c + n, c + n - T
+    i, j = np.arange(c, L)[:, None], np.arange(L)[None, :]
+    seen = np.where(i < U, j <= i, (j < U) | (j == i))
+    want, bound = np.zeros(q.shape), np.zeros(q.shape)
+    d = q.shape[2]
+    for h in range(q.shape[1]):
+        x = alpha * (q[:, h] @ k[:, h].T)
+        size = abs(alpha) * (np.abs(q[:, h]) @ np.abs(k[:, h]).T)
+        p = np.where(seen, x / (1.0 + np.exp(-x)), 0.0)
+        want[:, h] = p @ v[:, h] / N
+        off = np.where(seen, (np.abs(p) * (2.0 ** -8 + L * 2.0 ** -24) + np.abs(x) / 2 * 2.0 ** -10.9
+                              + 1.1 * (d + 2) * 2.0 ** -24 * size), 0.0)
+        bound[:, h] = off @ np.abs(v[:, h]) / N
+    return want, bound + (np.abs(want) + bound) * 2.0 ** -8 + 1e-38

@@ -99,3 +99,29 @@ def test_append_refusals(lib):
     for kw in (dict(page_size=12), dict(page_size=4), dict(page_size=2048), dict(head_stride=68), dict(k=(1 << 30) + 8),
                dict(page_stride=1 << 40)):
         assert _append(lib, _cache(**kw)) == UNSUPPORTED, kw
+
+
+def _attn(lib, cache=None, **kw):
+    a = dict(q=1 << 20, q_ld=128, off=1 << 12, kv=1 << 12, nt=None, B=2, H=2, d=64, total=16, max_new=8, max_kv=64, alpha=1.0,
+             N=16.0, out=1 << 24, out_ld=128)
+    a.update(kw)
+    vp = ctypes.c_void_p
+    c = _cache() if cache is None else cache
+    return lib.hstu_paged_attn_fwd(vp(a["q"]), a["q_ld"], ctypes.byref(c), vp(a["off"]), vp(a["kv"]), vp(a["nt"]), a["B"],
+                                   a["H"], a["d"], a["total"], a["max_new"], a["max_kv"], a["alpha"], a["N"], vp(a["out"]),
+                                   a["out_ld"], None)
+
+
+def test_attn_refusals(lib):
+    assert _attn(lib, total=0) == OK and _attn(lib, B=0) == OK
+    for kw in (dict(q=None), dict(out=None), dict(off=None), dict(kv=None), dict(B=-1), dict(H=0), dict(total=-1),
+               dict(max_new=-1), dict(max_kv=-1), dict(alpha=float("nan")), dict(alpha=float("inf")), dict(N=0.0),
+               dict(N=float("inf")), dict(q_ld=64), dict(out_ld=100), dict(out=1 << 20), dict(out=1 << 30),
+               dict(out=(1 << 31) + 64)):
+        assert _attn(lib, **kw) == INVALID, kw
+    for kw in (dict(d=16), dict(q=(1 << 20) + 2), dict(out=(1 << 24) + 8), dict(out_ld=129), dict(max_kv=2 ** 31 - 1)):
+        assert _attn(lib, **kw) == UNSUPPORTED, kw
+    for kw in (dict(v=None), dict(num_pages=0), dict(table_width=5)):
+        assert _attn(lib, _cache(**kw)) == INVALID, kw
+    for kw in (dict(page_size=24), dict(row_stride=129)):
+        assert _attn(lib, _cache(**kw)) == UNSUPPORTED, kw
