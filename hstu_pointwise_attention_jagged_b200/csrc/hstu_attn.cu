@@ -176,21 +176,6 @@ Plan carve(void* base, int32_t B) {
   return w;
 }
 
-int cost_bins(int32_t max_seq_len) {
-  // A 128-row item computes at most ceil(L/128) + 1 score tiles; the bins leave twice that room.
-  int64_t n = 2 * (static_cast<int64_t>(max_seq_len) / kTileRows + 3) + 1;
-  return static_cast<int>(n < kMaxCostBins ? n : kMaxCostBins);
-}
-
-// Waves a plan's keys need: those the batch's rows can reach, no more than the key space holds (the
-// plan kernels clear and scan waves x cost bins keys).
-int plan_waves(int64_t rows, int32_t wave_rows, int32_t nbins) {
-  const int64_t need = rows > 0 ? (rows + wave_rows - 1) / wave_rows : 1;
-  const int64_t fit = nbins > 0 ? kMaxCostBins / nbins : 1;
-  const int64_t n = need < fit ? need : fit;
-  return static_cast<int>(n > 0 ? n : 1);
-}
-
 // Scalar checks shared by every entry point.  Returns HSTU_OK or the status to report.
 hstu_status_t check_sizes(int32_t B, int32_t H, int32_t total_kv, int32_t total_q) {
   if (B < 0 || H < 1 || total_kv < 0 || total_q < 0 || total_q > total_kv) return HSTU_ERR_INVALID_ARGUMENT;
@@ -228,9 +213,7 @@ cudaError_t launch_plan(const int32_t* seq_offsets, const int32_t* num_targets, 
   a.max_seq_len = max_seq_len;
   a.nbins = cost_bins(max_seq_len);
   a.max_items = static_cast<int32_t>(capacity(B, H, total_q));
-  // Waves of users whose K and V (sized for d = 128: 512 bytes per row and head) take about a
-  // quarter of the 126 MB L2; as many waves as the key space allows.
-  a.wave_rows = static_cast<int32_t>((32ll << 20) / (512ll * H) > 0 ? (32ll << 20) / (512ll * H) : 1);
+  a.wave_rows = plan_wave_rows(H);  // as many waves as the key space allows
   a.nwaves = plan_waves(total_kv, a.wave_rows, a.nbins);
   a.q_start = w.q_start;
   a.block_start = w.block_start;
@@ -623,9 +606,8 @@ hstu_status_t run_bwd(const void* q, const void* k, const void* v, const void* d
   a.total = total;
   a.max_seq_len = max_seq_len;
   a.nbins = cost_bins(max_seq_len);
-  // Waves of users whose streamed pairs (Q and dO, or K and V: 512 bytes per row and head at
-  // d = 128) take about a quarter of L2.
-  a.wave_rows = static_cast<int32_t>((32ll << 20) / (512ll * H) > 0 ? (32ll << 20) / (512ll * H) : 1);
+  // Waves by the streamed pairs (Q and dO, or K and V).
+  a.wave_rows = plan_wave_rows(H);
   a.nwaves = plan_waves(total, a.wave_rows, a.nbins);
   a.max_items = static_cast<int32_t>(cap);
   a.header = header;

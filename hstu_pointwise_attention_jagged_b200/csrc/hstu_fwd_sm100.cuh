@@ -44,6 +44,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "paged_cache.cuh"
 #include "schedule.cuh"
 #include "sm100_ptx.cuh"
 
@@ -117,6 +118,7 @@ struct FwdParams {
   float inv_n;
   unsigned* err;
   uint64_t wait_limit_ns;      // limit of every pipeline wait (kWaitLimitNs; a self-check lowers it)
+  PagedFwd paged;              // paged form only; there q_start is q_offsets
 };
 
 template <int kStages>
@@ -127,8 +129,10 @@ struct SmemCtl {
   uint64_t o_full, o_empty;
   uint64_t sched_full[kSlots], sched_empty[kSlots];
   uint64_t drain;
-  // work slot: valid, h, kv_start, q_row0, pos0, nrows, L, U
-  int32_t slot[kSlots][8];
+  uint64_t v_tail;  // paged form: a V tile whose last rows are still to be cleared
+  // work slot: valid, h, kv_start, q_row0, pos0, nrows, L, U; paged form: tile0, tiles, parts, part
+  // too, and the first partial's slot in place of kv_start
+  int32_t slot[kSlots][12];
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -149,6 +153,13 @@ __device__ __forceinline__ Work read_slot(const volatile int32_t* s) {
   w.U = s[7];
   return w;
 }
+
+// The paged form's extra fields: this piece's tiles [tile0, tile0 + tiles) of its item's.
+struct Piece {
+  int tile0, tiles, parts, part;
+};
+
+__device__ __forceinline__ Piece read_piece(const volatile int32_t* s) { return Piece{s[8], s[9], s[10], s[11]}; }
 
 // Limits below this are test limits: their waits poll instead of suspending in try_wait, whose
 // suspension may last until the phase completes, so that the clock is read every few clocks.
@@ -192,6 +203,28 @@ static __device__ __noinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (!ptx::mbar_try_wait_for(bar, parity, (uint32_t)kDrainLimitNs))
     if (ptx::globaltimer_ns() - t0 > kDrainLimitNs) return;
+}
+
+// Abort path of the producer: lets every copy the CTA started land before its shared memory is
+// released.  A group barrier's phase completes once its bytes and the SiLU warps' arrivals are in,
+// and the arrivals of an aborted group may never come.  Arriving for them here is not an option: if
+// they did come while bytes were still outstanding, the extra arrival would land on a phase with no
+// arrivals pending, which is not defined.  So the producer only waits, on each barrier still in use,
+// all within one budget of kCopyGraceNs: every phase complete means every copy landed, and otherwise
+// the whole budget, a thousand times a copy's duration, has passed.  `loose`: a copy is on a barrier
+// whose phase cannot complete (its group was never armed), so the budget runs.
+template <class Ctl>
+__device__ __forceinline__ void drain_copies(Ctl* ctl, int g, int armed_hi, bool loose) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (int x = armed_hi > kGroupBars ? armed_hi - kGroupBars : 0; x < armed_hi; ++x) {
+    if (x >= g && x < 3) continue;  // group indices never used when the CTA had < 3 tiles
+    const uint32_t rb = ptx::smem_addr(&ctl->g_ready[x & (kGroupBars - 1)]);
+    const uint32_t par = (uint32_t)((x / kGroupBars) & 1);
+    while (!ptx::mbar_test_wait(rb, par) && ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
+    }
+  }
+  while (loose && ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -290,7 +323,196 @@ __device__ __forceinline__ void silu_tile(uint32_t taddr_s, float half_alpha, in
 // whole ring.)
 __device__ __forceinline__ int group_of_load(int e) { return e < 3 ? e : (e + 3) >> 1; }
 
-template <int D, bool kRab>
+// Producer of the paged form, run by the whole warp: the pages of a key tile are copied by as many lanes,
+// one each, whose table entries were read one tile ahead.  The order of the loads and the barriers are
+// the contiguous producer's (see the kernel below).
+//
+// A page the user does not have (past its length, or an entry outside the pool, which is reported) is
+// loaded from beyond the pool's last page, where the tensor map reads zeros; so a tile always
+// brings all its bytes.  Rows of the last page past the user's length may hold anything.  For K that
+// is harmless, their scores are masked by selection; for V it is not (0 * NaN), so such a V tile
+// lands on its own barrier, this warp clears the rows, and only then does the group become ready.
+template <int D, class Ctl>
+__device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                              const FwdParams& p, uint32_t sQ, uint32_t sKV, int lane) {
+  using Cfg = FwdCfg<D>;
+  volatile int32_t* abort_flag = &ctl->abort_flag;
+  auto bar = [](const uint64_t& b) { return ptx::smem_addr(&b); };
+  auto wait_all = [&](uint32_t b, uint32_t par) {
+    return (bool)__all_sync(0xffffffffu, wait_bounded(b, par, abort_flag, p.err, p.wait_limit_ns));
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const PagedView& cache = p.paged.cache;
+  const PagedPlan& plan = p.paged.plan;
+  const int ranges = plan.header[3];
+  int next = 0, last = 0;
+  if (ranges == 0) {
+    last = plan.header[1];
+  } else if ((int)blockIdx.x < ranges) {
+    next = plan.starts[blockIdx.x];
+    last = plan.starts[blockIdx.x + 1];
+  }
+  const int page_rows = 1 << cache.page_shift;
+  const int box_rows = page_rows < kTileRows ? page_rows : kTileRows;
+  const int boxes = kTileRows / box_rows;
+  const uint32_t box_off = (uint32_t)lane * box_rows * Cfg::kRowBytes;
+
+  // Where lane l's box of a tile comes from, and for V how many rows of the tile to keep.
+  struct Source {
+    int page, row, h, keep;
+  };
+  int slot = 0;
+  uint32_t sched_empty_par = (1u << kSlots) - 1u, tail_par = 0u;
+  int sub = 0, j = 0, g = 0, armed_hi = 0;
+  bool loose = false;
+  Source v0{}, v1{}, v2{};  // V tiles g-3, g-2, g-1
+  bool ok = true;
+  auto slot_free = [&](int e) {
+    if (e < Cfg::kStages) return true;
+    const int G = group_of_load(e - Cfg::kStages);
+    return wait_all(bar(ctl->s_full[G % kSCommits]), (uint32_t)((G / kSCommits) & 1));
+  };
+  auto copy = [&](const CUtensorMap* tm, uint32_t dst, uint32_t rb, const Source& s) {
+    if (lane < boxes) {
+      for (int blk = 0; blk < Cfg::kBlocks; ++blk)
+        ptx::tma_load_4d(dst + blk * Cfg::kBlockBytes + box_off, tm, rb, blk * Cfg::kBlockElems, s.row, s.h, s.page);
+    }
+  };
+  auto ring = [&](int e) { return sKV + (e % Cfg::kStages) * Cfg::kTileBytes; };
+  // The next V tile, the next K tile or both, in this order, onto the group barrier rb, and the producer's
+  // arrival there.
+  auto arm = [&](uint32_t rb, bool has_v, const Source v, bool has_k, const Source k) {
+    const uint32_t k_bytes = has_k ? Cfg::kTileBytes : 0u;
+    const bool clear = has_v && v.keep < kTileRows;
+    if (lane == 0) {
+      if (clear) {
+        if (k_bytes) ptx::mbar_expect_tx(rb, k_bytes);
+        ptx::mbar_arrive_expect_tx(bar(ctl->v_tail), Cfg::kTileBytes);
+      } else {
+        ptx::mbar_arrive_expect_tx(rb, k_bytes + (has_v ? Cfg::kTileBytes : 0u));
+        if (!has_v)  // no P.V in this group: stand in for the SiLU warps' arrivals
+          for (int a = 0; a < 4; ++a) ptx::mbar_arrive(rb);
+      }
+    }
+    __syncwarp();
+    const uint32_t vdst = ring(j);
+    if (has_v) {
+      copy(tm_v, vdst, clear ? bar(ctl->v_tail) : rb, v);
+      ++j;
+    }
+    if (has_k) {
+      copy(tm_k, ring(j), rb, k);
+      ++j;
+    }
+    if (clear) {
+      loose = true;
+      if (!wait_all(bar(ctl->v_tail), tail_par)) return false;
+      tail_par ^= 1u;
+      const uint32_t off = (uint32_t)v.keep * Cfg::kRowBytes;
+      for (uint32_t x = off + lane * 16; x < (uint32_t)Cfg::kBlockBytes; x += 32 * 16)
+        for (int blk = 0; blk < Cfg::kBlocks; ++blk) ptx::st_shared_v4(vdst + blk * Cfg::kBlockBytes + x, 0, 0, 0, 0);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(rb);
+    }
+    loose = false;
+    return true;
+  };
+
+  while (ok) {
+    int idx = next++;
+    if (ranges == 0) {
+      if (lane == 0) idx = atomicAdd(p.work_counter, 1);
+      idx = __shfl_sync(0xffffffffu, idx, 0);
+    }
+    const bool valid = idx < last;
+    PagedPiece pc{};
+    int q_row0 = 0, pos0 = 0, nrows = 0, L = 0, U = 0;
+    if (valid) {
+      const int4* at = reinterpret_cast<const int4*>(plan.pieces + idx);
+      const int4 a = at[0], b = at[1];
+      pc = PagedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      const int q0 = p.q_start[pc.b], n = p.q_start[pc.b + 1] - q0;
+      L = p.paged.kv_len[pc.b];
+      U = L - (p.num_targets ? p.num_targets[pc.b] : 0);
+      q_row0 = q0 + pc.block * kItemRows;
+      pos0 = L - n + pc.block * kItemRows;
+      nrows = min(n - pc.block * kItemRows, kItemRows);
+    }
+    if (!wait_all(bar(ctl->sched_empty[slot]), (sched_empty_par >> slot) & 1u)) {
+      ok = false;
+      break;
+    }
+    sched_empty_par ^= 1u << slot;
+    if (lane == 0) {
+      volatile int32_t* s = ctl->slot[slot];
+      s[0] = valid; s[1] = pc.h; s[2] = pc.slot; s[3] = q_row0;
+      s[4] = pos0; s[5] = nrows; s[6] = L; s[7] = U;
+      s[8] = pc.tile0; s[9] = pc.tiles; s[10] = pc.parts; s[11] = pc.part;
+      ptx::mbar_arrive(bar(ctl->sched_full[slot]));
+    }
+    slot = (slot + 1) & (kSlots - 1);
+    if (!valid) break;
+
+    const int32_t* table = cache.table + pc.b * cache.table_ld;
+    const TileRange r = key_tiles(pos0, pos0 + nrows, U);
+    auto source = [&](int k) {
+      const int key0 = tile_at(r, pc.tile0 + k) * kTileRows, key = key0 + lane * box_rows;
+      Source s;
+      s.h = pc.h;
+      s.row = key & (page_rows - 1);
+      s.page = cache.num_pages;
+      if (lane < boxes && key < L) {
+        const int page = table[key >> cache.page_shift];
+        if (page >= 0 && page < cache.num_pages) s.page = page;
+        else atomicOr(p.err, kErrBadOffsets);
+      }
+      // Whole pages past the length come as zeros already.
+      s.keep = L - key0 < kTileRows && (L & (box_rows - 1)) != 0 ? L - key0 : kTileRows;
+      return s;
+    };
+    Source ahead = source(0);
+    const int qb = sub % Cfg::kQBufs;
+    if (!wait_all(bar(ctl->q_empty[qb]), (uint32_t)(((sub / Cfg::kQBufs) & 1) ^ 1))) {
+      ok = false;
+      break;
+    }
+    loose = true;  // until group g is armed
+    if (lane == 0) {
+      const uint32_t rb = bar(ctl->g_ready[g & (kGroupBars - 1)]);
+      ptx::mbar_expect_tx(rb, Cfg::kTileBytes);
+      for (int blk = 0; blk < Cfg::kBlocks; ++blk)
+        ptx::tma_load_2d(sQ + qb * Cfg::kTileBytes + blk * Cfg::kBlockBytes, tm_q, rb, pc.h * D + blk * Cfg::kBlockElems,
+                         q_row0);
+    }
+    ++sub;
+    for (int k = 0; k < pc.tiles; ++k) {
+      const bool has_v = g >= 3;
+      if (!slot_free(j) || (has_v && !slot_free(j + 1))) { ok = false; break; }
+      const Source here = ahead;
+      if (k + 1 < pc.tiles) ahead = source(k + 1);
+      if (!arm(bar(ctl->g_ready[g & (kGroupBars - 1)]), has_v, v0, true, here)) { ok = false; break; }
+      v0 = v1;
+      v1 = v2;
+      v2 = here;
+      armed_hi = ++g;
+    }
+  }
+  // The closing groups t + 3 carry the V tiles of the last (up to) three score tiles t.
+  for (int t = (g >= 3 ? g - 3 : 0); t < g && ok; ++t) {
+    const int i = t - g + 3;  // 0, 1, 2 <-> tiles g-3, g-2, g-1
+    const Source v = i == 0 ? v0 : (i == 1 ? v1 : v2);
+    if (!slot_free(j)) { ok = false; break; }
+    if (!arm(bar(ctl->g_ready[(t + 3) & (kGroupBars - 1)]), true, v, false, v)) { ok = false; break; }
+    armed_hi = t + 4;
+  }
+  if (lane == 0 && *abort_flag) drain_copies(ctl, g, armed_hi, loose);
+}
+
+// kPaged: K and V come from a paged cache (tm_k, tm_v: 4-D maps of the pool) and the work from a
+// PagedPlan, whose pieces may be part of an item; produce_paged replaces the producer, and the
+// epilogue of a part writes fp32 sums.
+template <int D, bool kRab, bool kPaged = false>
 __global__ void __launch_bounds__(kNumThreads, 1)
     hstu_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -322,6 +544,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       ptx::mbar_init(bar(ctl->sched_empty[s]), 1 + 8 + 4);  // MMA, SiLU and epilogue warps
     }
     ptx::mbar_init(bar(ctl->drain), 1);
+    if constexpr (kPaged) ptx::mbar_init(bar(ctl->v_tail), 1);
     ctl->abort_flag = 0;
     ptx::fence_mbarrier_init();
     ptx::prefetch_tmap(&tm_q);
@@ -339,7 +562,9 @@ __global__ void __launch_bounds__(kNumThreads, 1)
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
-    if (lane == 0) {
+    if constexpr (kPaged) {
+      produce_paged<D>(ctl, &tm_q, &tm_k, &tm_v, p, sQ, sKV, lane);
+    } else if (lane == 0) {
       // Everything before this point touched only shared memory, TMEM and kernel parameters; the
       // plan (and q/k/v) come from the preceding grid.
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -454,25 +679,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         armed_hi = t + 4;
       }
       if (*abort_flag) {
-        // Let every copy this CTA started land before its shared memory is released.  A group
-        // barrier's phase completes once its bytes and the SiLU warps' arrivals are in, and the
-        // arrivals of an aborted group may never come.  Arriving for them here is not an option:
-        // if they did come while bytes were still outstanding, the extra arrival would land on a
-        // phase with no arrivals pending, which is not defined.  So the producer only waits, on
-        // each barrier still in use, all within one budget of kCopyGraceNs: every phase complete
-        // means every copy landed, and otherwise the whole budget, a thousand times a copy's
-        // duration, has passed.
-        const uint64_t t0 = ptx::globaltimer_ns();
-        for (int x = armed_hi > kGroupBars ? armed_hi - kGroupBars : 0; x < armed_hi; ++x) {
-          if (x >= g && x < 3) continue;  // group indices never used when the CTA had < 3 tiles
-          const uint32_t rb = bar(ctl->g_ready[x & (kGroupBars - 1)]);
-          const uint32_t par = (uint32_t)((x / kGroupBars) & 1);
-          while (!ptx::mbar_test_wait(rb, par) && ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
-          }
-        }
-        // A Q copy on a group that was never armed: that phase cannot complete, so the budget runs.
-        while (q_unarmed && ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
-        }
+        drain_copies(ctl, g, armed_hi, q_unarmed);
       }
     }
     __syncwarp();
@@ -531,6 +738,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       }
       sched_full_par ^= 1u << slot;
       const Work w = read_slot(ctl->slot[slot]);
+      const Piece pc = kPaged ? read_piece(ctl->slot[slot]) : Piece{};
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(ctl->sched_empty[slot]));
       slot = (slot + 1) & (kSlots - 1);
@@ -538,7 +746,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
 
       {
         const TileRange r = key_tiles(w.pos0, w.pos0 + w.nrows, w.U);
-        const int n = tile_count(r);
+        const int n = kPaged ? pc.tiles : tile_count(r);
         const int qb = sub % Cfg::kQBufs;
         const uint64_t dq = dq0 + ((qb * Cfg::kTileBytes) >> 4);
         for (int k = 0; k < n; ++k) {
@@ -603,6 +811,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       if (!ok) break;
       sched_full_par ^= 1u << slot;
       const Work w = read_slot(ctl->slot[slot]);
+      const Piece pc = kPaged ? read_piece(ctl->slot[slot]) : Piece{};
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(ctl->sched_empty[slot]));
       slot = (slot + 1) & (kSlots - 1);
@@ -613,7 +822,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       {
         const int p0 = w.pos0;
         const TileRange r = key_tiles(p0, p0 + w.nrows, w.U);
-        const int n = tile_count(r);
+        const int n = kPaged ? pc.tiles : tile_count(r);
         const int i_pos = p0 + row;                           // this thread's query position
         const int lim_abs = (i_pos < w.U) ? i_pos + 1 : w.U;  // keys [0, lim_abs) visible, plus self
         for (int k = (g + wg) & 1; k < n; k += 2) {
@@ -621,7 +830,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
           const int b = gt % 3;
           const uint32_t taddr_s = tmem + lane_off + Cfg::kColS + 128u * b;
           // The first chunk's biases do not depend on S: load them while S is computed.
-          const int j0 = tile_at(r, k) * kTileRows;
+          const int j0 = tile_at(r, kPaged ? pc.tile0 + k : k) * kTileRows;
           float bias[32];
           if constexpr (kRab) load_bias<0>(bias, rab_row, i_pos - j0, rab_max);
           ok = wait_bounded(bar(ctl->s_full[gt % kSCommits]), (uint32_t)((gt / kSCommits) & 1), abort_flag, p.err,
@@ -663,6 +872,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       if (!ok) break;
       sched_full_par ^= 1u << slot;
       const Work w = read_slot(ctl->slot[slot]);
+      const Piece pc = kPaged ? read_piece(ctl->slot[slot]) : Piece{};
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(ctl->sched_empty[slot]));
       slot = (slot + 1) & (kSlots - 1);
@@ -675,6 +885,53 @@ __global__ void __launch_bounds__(kNumThreads, 1)
         if (!ok) break;
         o_full_par ^= 1u;
         ptx::tc_fence_after();
+        if (kPaged && pc.parts > 1) {
+          // A piece of a cut item: its sums go to its partial.  The warp that finishes an item's last
+          // quarter adds the partials of that quarter in piece order, so the result does not depend on
+          // which piece that was.
+          const int first = w.kv_start;  // slot of part 0
+          float4* mine = p.paged.partials + (size_t)(first + pc.part) * (D / 4) * kTileRows + row;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ro[32];
+            ptx::tmem_ld32(taddr_o + c * 32, ro);
+            ptx::tmem_ld_wait(ro);
+            if (row < nr) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                __stcg(mine + (c * 8 + e) * kTileRows,
+                       make_float4(__uint_as_float(ro[4 * e]), __uint_as_float(ro[4 * e + 1]),
+                                   __uint_as_float(ro[4 * e + 2]), __uint_as_float(ro[4 * e + 3])));
+            }
+          }
+          ptx::tc_fence_before();
+          __threadfence();
+          __syncwarp();
+          int finished = 0;
+          if (lane == 0) {
+            ptx::mbar_arrive(bar(ctl->o_empty));
+            finished = atomicAdd(p.paged.plan.done + first * 4 + quarter, 1);
+          }
+          finished = __shfl_sync(0xffffffffu, finished, 0);
+          if (finished == pc.parts - 1 && row < nr) {
+            __threadfence();
+            const float4* sums = p.paged.partials + (size_t)first * (D / 4) * kTileRows + row;
+            uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)(w.q_row0 + row) * p.out_ld + (size_t)w.h * D);
+#pragma unroll 2
+            for (int c = 0; c < D / 8; ++c) {
+              float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+              for (int k = 0; k < pc.parts; ++k) {
+                const float4 a0 = __ldcg(sums + (k * (D / 4) + 2 * c) * kTileRows);
+                const float4 a1 = __ldcg(sums + (k * (D / 4) + 2 * c + 1) * kTileRows);
+                s0.x += a0.x; s0.y += a0.y; s0.z += a0.z; s0.w += a0.w;
+                s1.x += a1.x; s1.y += a1.y; s1.z += a1.z; s1.w += a1.w;
+              }
+              dst[c] = make_uint4(pack_bf16x2(s0.x * inv_n, s0.y * inv_n), pack_bf16x2(s0.z * inv_n, s0.w * inv_n),
+                                  pack_bf16x2(s1.x * inv_n, s1.y * inv_n), pack_bf16x2(s1.z * inv_n, s1.w * inv_n));
+            }
+          }
+          continue;
+        }
         // O * (1/N) -> bf16 pairs in registers; O is then released to the next query tile's P.V.
         uint32_t a[D / 2];
 #pragma unroll

@@ -13,6 +13,7 @@
 #include "hstu_paged.h"
 #include "paged_cache.cuh"
 #include "paged_rows_sm100.cuh"
+#include "paged_schedule.cuh"
 #include "rotary_sm100.cuh"
 
 namespace hstu {
@@ -178,6 +179,125 @@ hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t
   return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D>, a) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+
+// 4-D map of the pool: columns, rows of a page, heads, pages; the box is one page's rows, at most a tile's.
+bool encode_pool(CUtensorMap* map, const void* base, const hstu_paged_cache_t& c, int32_t H, int32_t d) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.row_stride) * 2, static_cast<cuuint64_t>(c.head_stride) * 2,
+                                 static_cast<cuuint64_t>(c.page_stride) * 2};
+  const cuuint32_t box[4] = {d >= 64 ? 64u : 32u,
+                             static_cast<cuuint32_t>(c.page_size < kTileRows ? c.page_size : kTileRows), 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUtensorMapSwizzle swz = d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_q(CUtensorMap* map, const void* base, int64_t rows, int64_t width, int64_t ld, int32_t d) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {d >= 64 ? 64u : 32u, static_cast<cuuint32_t>(kTileRows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUtensorMapSwizzle swz = d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Many rows a user: the plan, then the tcgen05 kernel, over one buffer from the library's pool.
+template <int D>
+hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, float alpha, DeviceState& st,
+                          cudaStream_t stream) {
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64 || !tensor_map_encoder()) return HSTU_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  std::call_once(once[dev], [&] {
+    e = cudaFuncSetAttribute(hstu_fwd_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             FwdCfg<D>::kSmemBytes);
+  });
+  if (e != cudaSuccess) return HSTU_ERR_CUDA;
+  const int ctas = st.num_sms;
+  const int64_t capacity = static_cast<int64_t>(a.H) * (a.total_new / kItemRows + a.B);
+  if (capacity + ctas > INT_MAX / 2) return HSTU_ERR_UNSUPPORTED;
+  const int64_t width = static_cast<int64_t>(a.H) * D;
+  CUtensorMap tq, tk, tv;
+  if (!encode_q(&tq, a.q, a.total_new, width, a.q_ld, D) || !encode_pool(&tk, cache.k, cache, a.H, D) ||
+      !encode_pool(&tv, cache.v, cache, a.H, D))
+    return HSTU_ERR_CUDA;
+  // header | block_start | starts | done | pieces | partials
+  const size_t o_block = 256, o_starts = o_block + pad256((static_cast<size_t>(a.B) + 1) * 4),
+               o_done = o_starts + pad256((ctas + 1) * 4), o_pieces = o_done + pad256(8 * ctas * 4),
+               o_partials = o_pieces + pad256((capacity + ctas) * sizeof(PagedPiece)),
+               bytes = o_partials + static_cast<size_t>(2 * ctas) * kTileRows * D * 4;
+  void* buf = nullptr;
+  if (cudaMallocFromPoolAsync(&buf, bytes, st.pool, stream) != cudaSuccess) return HSTU_ERR_CUDA;
+  uint8_t* at = static_cast<uint8_t*>(buf);
+  PagedSchedArgs s;
+  s.cache = a.cache;
+  s.q_offsets = a.q_offsets;
+  s.kv_len = a.kv_len;
+  s.num_targets = a.num_targets;
+  s.B = a.B;
+  s.H = a.H;
+  s.total_new = a.total_new;
+  s.max_new = a.max_new;
+  s.max_kv = a.max_kv;
+  s.nbins = cost_bins(a.max_kv);
+  s.wave_rows = plan_wave_rows(a.H);
+  s.nwaves = plan_waves(static_cast<int64_t>(a.B) * a.max_kv, s.wave_rows, s.nbins);
+  s.num_ctas = ctas;
+  s.max_pieces = static_cast<int32_t>(capacity + ctas);
+  s.plan.header = reinterpret_cast<int32_t*>(at);
+  s.plan.block_start = reinterpret_cast<int32_t*>(at + o_block);
+  s.plan.starts = reinterpret_cast<int32_t*>(at + o_starts);
+  s.plan.done = reinterpret_cast<int32_t*>(at + o_done);
+  s.plan.pieces = reinterpret_cast<PagedPiece*>(at + o_pieces);
+  s.err = a.err;
+  FwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.num_targets = a.num_targets;
+  p.q_start = a.q_offsets;
+  p.work_counter = s.plan.header;
+  p.done_counter = s.plan.header + 2;
+  p.out = a.out;
+  p.out_ld = a.out_ld;
+  p.H = a.H;
+  p.half_alpha = 0.5f * alpha;
+  p.inv_n = a.inv_n;
+  p.err = a.err;
+  p.wait_limit_ns = kWaitLimitNs;
+  p.paged.cache = a.cache;
+  p.paged.kv_len = a.kv_len;
+  p.paged.plan = s.plan;
+  p.paged.partials = reinterpret_cast<float4*>(at + o_partials);
+  e = launch_dependent(paged_schedule_kernel, 1, kSchedThreads, 0, stream, s);
+  if (e == cudaSuccess)
+    e = launch_dependent(hstu_fwd_kernel<D, false, true>, ctas, kNumThreads, FwdCfg<D>::kSmemBytes, stream, tq, tk, tv, p);
+  if (cudaFreeAsync(buf, stream) != cudaSuccess && e == cudaSuccess) return HSTU_ERR_CUDA;
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace hstu
 
@@ -304,6 +424,9 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
   a.inv_n = 1.0f / N;
   a.err = st->err_word;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (most > kRowsBlock)
+    return d == 128 ? launch_many<128>(a, *cache, alpha, *st, cs)
+                    : (d == 64 ? launch_many<64>(a, *cache, alpha, *st, cs) : launch_many<32>(a, *cache, alpha, *st, cs));
   return d == 128 ? launch_rows<128>(a, *st, cs) : (d == 64 ? launch_rows<64>(a, *st, cs) : launch_rows<32>(a, *st, cs));
 }
 

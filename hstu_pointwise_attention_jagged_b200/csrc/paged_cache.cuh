@@ -1,5 +1,5 @@
-// paged_cache.cuh — device view of the paged K/V cache (hstu_paged_cache_t) and the checks of one
-// user's lengths that every kernel on it makes.
+// paged_cache.cuh — device view of the paged K/V cache (hstu_paged_cache_t), the checks of one user's
+// lengths that every kernel on it makes, and the work plan of the many-row attention.
 #pragma once
 
 #include <cstdint>
@@ -40,5 +40,27 @@ __device__ __forceinline__ PagedUser paged_user(const PagedView& c, const int32_
          (u.n == 0 || ((static_cast<int64_t>(u.L) + (1 << c.page_shift) - 1) >> c.page_shift) <= c.table_width);
   return u;
 }
+
+struct PagedPiece {
+  int32_t b, block, h, parts;          // parts: pieces of the item (1: whole)
+  int32_t tile0, tiles, slot, part;    // tiles [tile0, tile0 + tiles) of the item's; slot: first partial of the item
+};
+static_assert(sizeof(PagedPiece) == 32, "two 16-byte loads");
+
+struct PagedPlan {
+  int32_t* header;       // [8] {queue counter, pieces, finished CTAs, ranges (0: queue), partials used, 0, 0, 0}
+  int32_t* block_start;  // [B+1] first block of each user
+  int32_t* starts;       // [num_ctas+1] first piece of each range
+  int32_t* done;         // [4 * 2 * num_ctas] finished pieces of a cut item, for each quarter of its rows
+  PagedPiece* pieces;    // [max_pieces]
+};
+
+// The paged form of the forward kernel's parameters.
+struct PagedFwd {
+  PagedView cache;
+  const int32_t* kv_len;
+  PagedPlan plan;
+  float4* partials;  // [slot][D / 4][128 rows]: fp32 sums of the pieces of cut items
+};
 
 }  // namespace hstu

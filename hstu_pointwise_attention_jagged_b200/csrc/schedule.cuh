@@ -71,6 +71,29 @@ constexpr int kSchedWarps = kSchedThreads / 32;
 constexpr int kMaxCostBins = 4096;
 constexpr int kCachedUsers = 256;  // batches up to this many users keep per-user values in shared memory
 
+// Cost bins a plan needs.  A 128-row item computes at most ceil(L/128) + 1 score tiles; the bins
+// leave twice that room.
+inline int cost_bins(int32_t max_seq_len) {
+  const int64_t n = 2 * (static_cast<int64_t>(max_seq_len) / kTileRows + 3) + 1;
+  return static_cast<int>(n < kMaxCostBins ? n : kMaxCostBins);
+}
+
+// Waves a plan's keys need: those the batch's rows can reach, no more than the key space holds (the
+// plan kernels clear and scan waves x cost bins keys).
+inline int plan_waves(int64_t rows, int32_t wave_rows, int32_t nbins) {
+  const int64_t need = rows > 0 ? (rows + wave_rows - 1) / wave_rows : 1;
+  const int64_t fit = nbins > 0 ? kMaxCostBins / nbins : 1;
+  const int64_t n = need < fit ? need : fit;
+  return static_cast<int>(n > 0 ? n : 1);
+}
+
+// Rows of a wave: users whose K and V (sized for d = 128: 512 bytes per row and head) take about a
+// quarter of the 126 MB L2.
+inline int32_t plan_wave_rows(int32_t H) {
+  const int64_t n = (32ll << 20) / (512ll * H);
+  return static_cast<int32_t>(n > 0 ? n : 1);
+}
+
 struct SchedArgs {
   const int32_t* seq_offsets;  // [B+1]
   const int32_t* num_targets;  // [B] or null
