@@ -24,5 +24,6 @@ def __getattr__(name):
         return getattr(binding, name)
     if name in _PAGED_NAMES:
         from . import paged
-        return getattr(paged, name)
+        globals()[name] = value = getattr(paged, name)  # the next use skips this lookup
+        return value
     raise AttributeError(name)

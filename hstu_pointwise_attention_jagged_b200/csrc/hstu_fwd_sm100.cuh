@@ -130,9 +130,9 @@ struct SmemCtl {
   uint64_t sched_full[kSlots], sched_empty[kSlots];
   uint64_t drain;
   uint64_t v_tail;  // paged form: a V tile whose last rows are still to be cleared
-  // work slot: valid, h, kv_start, q_row0, pos0, nrows, L, U; paged form: tile0, tiles, parts, part
-  // too, and the first partial's slot in place of kv_start
-  int32_t slot[kSlots][12];
+  // work slot: valid, h, kv_start, q_row0, pos0, nrows, L, U; paged form: tile0, tiles, parts, part,
+  // pitch too, and the queue place of the item's first part in place of kv_start
+  int32_t slot[kSlots][13];
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -156,10 +156,10 @@ __device__ __forceinline__ Work read_slot(const volatile int32_t* s) {
 
 // The paged form's extra fields: this piece's tiles [tile0, tile0 + tiles) of its item's.
 struct Piece {
-  int tile0, tiles, parts, part;
+  int tile0, tiles, parts, part, pitch;
 };
 
-__device__ __forceinline__ Piece read_piece(const volatile int32_t* s) { return Piece{s[8], s[9], s[10], s[11]}; }
+__device__ __forceinline__ Piece read_piece(const volatile int32_t* s) { return Piece{s[8], s[9], s[10], s[11], s[12]}; }
 
 // Limits below this are test limits: their waits poll instead of suspending in try_wait, whose
 // suspension may last until the phase completes, so that the clock is read every few clocks.
@@ -344,22 +344,17 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedView& cache = p.paged.cache;
   const PagedPlan& plan = p.paged.plan;
-  const int ranges = plan.header[3];
-  int next = 0, last = 0;
-  if (ranges == 0) {
-    last = plan.header[1];
-  } else if ((int)blockIdx.x < ranges) {
-    next = plan.starts[blockIdx.x];
-    last = plan.starts[blockIdx.x + 1];
-  }
+  const int M = plan.header[1];
   const int page_rows = 1 << cache.page_shift;
   const int box_rows = page_rows < kTileRows ? page_rows : kTileRows;
   const int boxes = kTileRows / box_rows;
   const uint32_t box_off = (uint32_t)lane * box_rows * Cfg::kRowBytes;
 
-  // Where lane l's box of a tile comes from, and for V how many rows of the tile to keep.
+  // Where lane l's box of a tile comes from (held: the user has that page), and for V how many rows of
+  // the tile to keep.
   struct Source {
     int page, row, h, keep;
+    bool held;
   };
   int slot = 0;
   uint32_t sched_empty_par = (1u << kSlots) - 1u, tail_par = 0u;
@@ -420,18 +415,17 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
   };
 
   while (ok) {
-    int idx = next++;
-    if (ranges == 0) {
-      if (lane == 0) idx = atomicAdd(p.work_counter, 1);
-      idx = __shfl_sync(0xffffffffu, idx, 0);
-    }
-    const bool valid = idx < last;
+    int idx = 0;
+    if (lane == 0) idx = atomicAdd(p.work_counter, 1);
+    idx = __shfl_sync(0xffffffffu, idx, 0);
+    const bool valid = idx < M;
     PagedPiece pc{};
     int q_row0 = 0, pos0 = 0, nrows = 0, L = 0, U = 0;
     if (valid) {
       const int4* at = reinterpret_cast<const int4*>(plan.pieces + idx);
       const int4 a = at[0], b = at[1];
       pc = PagedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      if (pc.tiles == 0) continue;
       const int q0 = p.q_start[pc.b], n = p.q_start[pc.b + 1] - q0;
       L = p.paged.kv_len[pc.b];
       U = L - (p.num_targets ? p.num_targets[pc.b] : 0);
@@ -446,9 +440,10 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
     sched_empty_par ^= 1u << slot;
     if (lane == 0) {
       volatile int32_t* s = ctl->slot[slot];
-      s[0] = valid; s[1] = pc.h; s[2] = pc.slot; s[3] = q_row0;
+      s[0] = valid; s[1] = pc.h; s[2] = idx - pc.part * pc.pitch; s[3] = q_row0;
       s[4] = pos0; s[5] = nrows; s[6] = L; s[7] = U;
       s[8] = pc.tile0; s[9] = pc.tiles; s[10] = pc.parts; s[11] = pc.part;
+      s[12] = pc.pitch;
       ptx::mbar_arrive(bar(ctl->sched_full[slot]));
     }
     slot = (slot + 1) & (kSlots - 1);
@@ -456,17 +451,15 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
 
     const int32_t* table = cache.table + pc.b * cache.table_ld;
     const TileRange r = key_tiles(pos0, pos0 + nrows, U);
+    // Only loads the table entry: it is looked at when the tile's turn comes.
     auto source = [&](int k) {
       const int key0 = tile_at(r, pc.tile0 + k) * kTileRows, key = key0 + lane * box_rows;
       Source s;
       s.h = pc.h;
       s.row = key & (page_rows - 1);
+      s.held = lane < boxes && key < L;
       s.page = cache.num_pages;
-      if (lane < boxes && key < L) {
-        const int page = table[key >> cache.page_shift];
-        if (page >= 0 && page < cache.num_pages) s.page = page;
-        else atomicOr(p.err, kErrBadOffsets);
-      }
+      if (s.held) s.page = table[key >> cache.page_shift];
       // Whole pages past the length come as zeros already.
       s.keep = L - key0 < kTileRows && (L & (box_rows - 1)) != 0 ? L - key0 : kTileRows;
       return s;
@@ -489,8 +482,12 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
     for (int k = 0; k < pc.tiles; ++k) {
       const bool has_v = g >= 3;
       if (!slot_free(j) || (has_v && !slot_free(j + 1))) { ok = false; break; }
-      const Source here = ahead;
+      Source here = ahead;
       if (k + 1 < pc.tiles) ahead = source(k + 1);
+      if (here.held && (unsigned)here.page >= (unsigned)cache.num_pages) {
+        atomicOr(p.err, kErrBadOffsets);
+        here.page = cache.num_pages;
+      }
       if (!arm(bar(ctl->g_ready[g & (kGroupBars - 1)]), has_v, v0, true, here)) { ok = false; break; }
       v0 = v1;
       v1 = v2;
@@ -889,8 +886,10 @@ __global__ void __launch_bounds__(kNumThreads, 1)
           // A piece of a cut item: its sums go to its partial.  The warp that finishes an item's last
           // quarter adds the partials of that quarter in piece order, so the result does not depend on
           // which piece that was.
-          const int first = w.kv_start;  // slot of part 0
-          float4* mine = p.paged.partials + (size_t)(first + pc.part) * (D / 4) * kTileRows + row;
+          const int first = w.kv_start;  // queue place of part 0
+          const size_t part_quads = (size_t)pc.pitch * (D / 4) * kTileRows;  // between two parts' sums
+          float4* sums = p.paged.partials + (size_t)first * (D / 4) * kTileRows + row;
+          float4* mine = sums + pc.part * part_quads;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ro[32];
@@ -905,29 +904,40 @@ __global__ void __launch_bounds__(kNumThreads, 1)
             }
           }
           ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(ctl->o_empty));
           __threadfence();
           __syncwarp();
           int finished = 0;
-          if (lane == 0) {
-            ptx::mbar_arrive(bar(ctl->o_empty));
-            finished = atomicAdd(p.paged.plan.done + first * 4 + quarter, 1);
-          }
+          if (lane == 0) finished = atomicAdd(p.paged.plan.done + first * 4 + quarter, 1);
           finished = __shfl_sync(0xffffffffu, finished, 0);
           if (finished == pc.parts - 1 && row < nr) {
             __threadfence();
-            const float4* sums = p.paged.partials + (size_t)first * (D / 4) * kTileRows + row;
             uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)(w.q_row0 + row) * p.out_ld + (size_t)w.h * D);
+            // 32 columns at a time, two parts' loads in flight: the sum is bound by their latency.
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float acc[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) acc[e] = 0.0f;
+              const float4* from = sums + c * 8 * kTileRows;
 #pragma unroll 2
-            for (int c = 0; c < D / 8; ++c) {
-              float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
               for (int k = 0; k < pc.parts; ++k) {
-                const float4 a0 = __ldcg(sums + (k * (D / 4) + 2 * c) * kTileRows);
-                const float4 a1 = __ldcg(sums + (k * (D / 4) + 2 * c + 1) * kTileRows);
-                s0.x += a0.x; s0.y += a0.y; s0.z += a0.z; s0.w += a0.w;
-                s1.x += a1.x; s1.y += a1.y; s1.z += a1.z; s1.w += a1.w;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 v = __ldcg(from + k * part_quads + e * kTileRows);
+                  acc[4 * e] += v.x;
+                  acc[4 * e + 1] += v.y;
+                  acc[4 * e + 2] += v.z;
+                  acc[4 * e + 3] += v.w;
+                }
               }
-              dst[c] = make_uint4(pack_bf16x2(s0.x * inv_n, s0.y * inv_n), pack_bf16x2(s0.z * inv_n, s0.w * inv_n),
-                                  pack_bf16x2(s1.x * inv_n, s1.y * inv_n), pack_bf16x2(s1.z * inv_n, s1.w * inv_n));
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                dst[c * 4 + e] = make_uint4(pack_bf16x2(acc[8 * e] * inv_n, acc[8 * e + 1] * inv_n),
+                                            pack_bf16x2(acc[8 * e + 2] * inv_n, acc[8 * e + 3] * inv_n),
+                                            pack_bf16x2(acc[8 * e + 4] * inv_n, acc[8 * e + 5] * inv_n),
+                                            pack_bf16x2(acc[8 * e + 6] * inv_n, acc[8 * e + 7] * inv_n));
             }
           }
           continue;

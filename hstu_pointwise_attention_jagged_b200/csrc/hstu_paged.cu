@@ -239,17 +239,19 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   if (e != cudaSuccess) return HSTU_ERR_CUDA;
   const int ctas = st.num_sms;
   const int64_t capacity = static_cast<int64_t>(a.H) * (a.total_new / kItemRows + a.B);
-  if (capacity + ctas > INT_MAX / 2) return HSTU_ERR_UNSUPPORTED;
+  if (capacity > INT_MAX / 2) return HSTU_ERR_UNSUPPORTED;
   const int64_t width = static_cast<int64_t>(a.H) * D;
   CUtensorMap tq, tk, tv;
   if (!encode_q(&tq, a.q, a.total_new, width, a.q_ld, D) || !encode_pool(&tk, cache.k, cache, a.H, D) ||
       !encode_pool(&tv, cache.v, cache, a.H, D))
     return HSTU_ERR_CUDA;
-  // header | block_start | starts | done | pieces | partials
-  const size_t o_block = 256, o_starts = o_block + pad256((static_cast<size_t>(a.B) + 1) * 4),
-               o_done = o_starts + pad256((ctas + 1) * 4), o_pieces = o_done + pad256(8 * ctas * 4),
-               o_partials = o_pieces + pad256((capacity + ctas) * sizeof(PagedPiece)),
-               bytes = o_partials + static_cast<size_t>(2 * ctas) * kTileRows * D * 4;
+  // header | block_start | done | pieces | partials; items are cut in batches that the plan kernel
+  // keeps on chip, into at most max_cut pieces.
+  const int64_t max_cut = a.B <= kCachedUsers ? kMaxCutRounds * ctas : 0;
+  const size_t o_block = 256, o_done = o_block + pad256((static_cast<size_t>(a.B) + 1) * 4),
+               o_pieces = o_done + pad256(4 * max_cut * 4),
+               o_partials = o_pieces + pad256((capacity > max_cut ? capacity : max_cut) * sizeof(PagedPiece)),
+               bytes = o_partials + static_cast<size_t>(max_cut) * kTileRows * D * 4;
   void* buf = nullptr;
   if (cudaMallocFromPoolAsync(&buf, bytes, st.pool, stream) != cudaSuccess) return HSTU_ERR_CUDA;
   uint8_t* at = static_cast<uint8_t*>(buf);
@@ -267,10 +269,10 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   s.wave_rows = plan_wave_rows(a.H);
   s.nwaves = plan_waves(static_cast<int64_t>(a.B) * a.max_kv, s.wave_rows, s.nbins);
   s.num_ctas = ctas;
-  s.max_pieces = static_cast<int32_t>(capacity + ctas);
+  s.max_items = static_cast<int32_t>(capacity);
+  s.max_cut = static_cast<int32_t>(max_cut);
   s.plan.header = reinterpret_cast<int32_t*>(at);
   s.plan.block_start = reinterpret_cast<int32_t*>(at + o_block);
-  s.plan.starts = reinterpret_cast<int32_t*>(at + o_starts);
   s.plan.done = reinterpret_cast<int32_t*>(at + o_done);
   s.plan.pieces = reinterpret_cast<PagedPiece*>(at + o_pieces);
   s.err = a.err;

@@ -42,17 +42,18 @@ __device__ __forceinline__ PagedUser paged_user(const PagedView& c, const int32_
 }
 
 struct PagedPiece {
-  int32_t b, block, h, parts;          // parts: pieces of the item (1: whole)
-  int32_t tile0, tiles, slot, part;    // tiles [tile0, tile0 + tiles) of the item's; slot: first partial of the item
+  int32_t b, block, h;
+  int32_t tile0, tiles;  // tiles [tile0, tile0 + tiles) of the item's; tiles = 0: nothing to do
+  int32_t parts, part;   // pieces of the item (1: whole) and which one this is
+  int32_t pitch;         // queue places between the item's pieces
 };
 static_assert(sizeof(PagedPiece) == 32, "two 16-byte loads");
 
 struct PagedPlan {
-  int32_t* header;       // [8] {queue counter, pieces, finished CTAs, ranges (0: queue), partials used, 0, 0, 0}
+  int32_t* header;       // [8] {queue counter, pieces, finished CTAs, cuts, 0, 0, 0, 0}
   int32_t* block_start;  // [B+1] first block of each user
-  int32_t* starts;       // [num_ctas+1] first piece of each range
-  int32_t* done;         // [4 * 2 * num_ctas] finished pieces of a cut item, for each quarter of its rows
-  PagedPiece* pieces;    // [max_pieces]
+  int32_t* done;         // [4 * max_cut] finished pieces of a cut item, for each quarter of its rows
+  PagedPiece* pieces;    // [max_pieces] the queue
 };
 
 // The paged form of the forward kernel's parameters.
@@ -60,7 +61,7 @@ struct PagedFwd {
   PagedView cache;
   const int32_t* kv_len;
   PagedPlan plan;
-  float4* partials;  // [slot][D / 4][128 rows]: fp32 sums of the pieces of cut items
+  float4* partials;  // [queue place][D / 4][128 rows]: fp32 sums of the pieces of cut items
 };
 
 }  // namespace hstu

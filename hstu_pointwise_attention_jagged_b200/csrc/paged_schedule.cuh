@@ -1,14 +1,13 @@
 // paged_schedule.cuh — work plan of the many-row paged attention (the paged form of hstu_fwd_kernel).
 //
-// The unit of work is a piece: some consecutive key tiles of one item (user, head, 128 query rows).
-// Two forms, chosen on the device from the number of items:
-//   queue    many items for the CTAs: every piece is a whole item, taken from a queue in waves of users
-//            whose K and V fit a quarter of L2, by non-increasing cost within a wave (schedule.cuh).
-//   ranges   few items: the tiles of all items, in item order, are dealt out in equal runs, one for each CTA,
-//            and an item that a boundary falls into is cut there.  Whole items would leave SMs
-//            idle: 192 items of 26 tiles on 148 SMs take 52 tiles' time, the runs take 34.  The
-//            pieces of a cut item leave fp32 partial outputs, and the last one to finish adds them
-//            up in piece order (hstu_fwd_sm100.cuh, epilogue).
+// The unit of work is a piece: some consecutive key tiles of one item (user, head, 128 query rows), taken
+// from a queue by the CTAs.  With many items every piece is a whole item, in waves of users whose
+// K and V fit a quarter of L2, by non-increasing cost within a wave (schedule.cuh).  With few items for the
+// CTAs, whole items can leave SMs idle: 192 items of 26 tiles on 148 SMs take the time of 52 tiles, where
+// 34 would do.  So the plan may cut items into pieces of at most q tiles, choosing q by the
+// estimate rounds * (q + overhead).  The pieces of a cut item leave fp32 partial outputs, and the last one to
+// finish adds them up in order (hstu_fwd_sm100.cuh, epilogue).  Pieces of one key range of one user and head
+// are neighbours in the queue: CTAs that work side by side read the same K and V.
 #pragma once
 
 #include <climits>
@@ -19,41 +18,29 @@
 
 namespace hstu {
 
-constexpr int kRangeItemsPerCta = 8;    // fewer items than this for each CTA: ranges
-constexpr int kMaxRangeItems = 2048;    // ... if the items fit the tables below
-constexpr int kMinRangeTiles = 4;       // a run is at least this long (the sums of a shorter one cost more than it does)
+constexpr int kMaxCutRounds = 4;  // cut items make at most this many pieces for each CTA
+constexpr int kMaxCuts = 16;      // pieces of the longest item
+constexpr int kMinPieceTiles = 2;
+constexpr int kPieceOverhead = 3; // tiles: filling the pipeline, writing and adding the partial
 
 struct PagedSchedArgs {
   PagedView cache;
   const int32_t* q_offsets;
   const int32_t* kv_len;
   const int32_t* num_targets;
-  int32_t B, H, total_new, max_new, max_kv, nbins, nwaves, wave_rows, num_ctas, max_pieces;
+  int32_t B, H, total_new, max_new, max_kv, nbins, nwaves, wave_rows, num_ctas, max_items, max_cut;
   PagedPlan plan;
   unsigned* err;
 };
-
-// First tile of range r when `tiles` tiles are dealt out in `ranges` runs; ranges <= tiles, so none is empty.
-__device__ __forceinline__ int range_begin(int tiles, int ranges, int r) {
-  return (int)((int64_t)tiles * r / ranges);
-}
-// Range that tile x falls into.
-__device__ __forceinline__ int range_of(int tiles, int ranges, int x) {
-  int r = (int)((int64_t)x * ranges / tiles);
-  while (r + 1 < ranges && range_begin(tiles, ranges, r + 1) <= x) ++r;
-  while (r > 0 && range_begin(tiles, ranges, r) > x) --r;
-  return r;
-}
 
 // One CTA of kSchedThreads threads.
 __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const PagedSchedArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int hist[kMaxCostBins];
-  __shared__ int cum[kMaxRangeItems];
   __shared__ long long scan_scratch[2][32];
   __shared__ long long carry_blocks, carry_rows;
-  __shared__ int slots;
+  __shared__ int longest, pieces_of[kMaxCuts + 1];
   __shared__ PagedUser s_user[kCachedUsers];
   __shared__ int s_start[kCachedUsers + 1], s_wave[kCachedUsers];
   const bool cached = a.B <= kCachedUsers;
@@ -61,9 +48,9 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   if (tid == 0) {
     carry_blocks = 0;
     carry_rows = 0;
-    slots = 0;
+    longest = 0;
   }
-  for (int i = tid; i < kMaxCostBins; i += kSchedThreads) hist[i] = 0;
+  if (tid <= kMaxCuts) pieces_of[tid] = 0;
   __syncthreads();
 
   // Pass 1: check every user; prefix sums of 128-row blocks and of cached rows.
@@ -106,10 +93,11 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     if (cached) s_start[a.B] = nblocks;
   }
   __syncthreads();
-  // Block g: its user, index within the user and tiles.  Overlapping (inconsistent) offsets can make
-  // the users' blocks more than the plan has room for; the surplus is dropped, and was reported.
+  // Overlapping (inconsistent) offsets can make the users' blocks more than the plan has room for; the
+  // surplus is dropped, and was reported.
   const int64_t items64 = (int64_t)nblocks * a.H;
-  const int items = (int)(items64 < a.max_pieces - a.num_ctas ? items64 : a.max_pieces - a.num_ctas);
+  const int items = (int)(items64 < a.max_items ? items64 : a.max_items);
+  // Block g: its user, index within the user and tiles.
   auto block_of = [&](int g, int& b, int& blk) {
     b = owner_of(cached ? s_start : a.plan.block_start, a.B, g);
     blk = g - (cached ? s_start[b] : a.plan.block_start[b]);
@@ -120,77 +108,83 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     return item_cost(u.L - u.n + blk * kItemRows, rows < kItemRows ? rows : kItemRows, u.L - u.T);
   };
 
-  if (items < kRangeItemsPerCta * a.num_ctas && items <= kMaxRangeItems &&
-      (int64_t)items * (a.max_kv / kTileRows + 2) < INT_MAX) {
-    // ------------------------------------------------------------------ ranges
-    // Items in the order (user, head, block): neighbours read the same K and V.
-    auto item_of = [&](int i, int& b, int& blk, int& h) {
-      // The user's first item is H times its first block; within it heads, then blocks.
-      b = owner_of(cached ? s_start : a.plan.block_start, a.B, i / a.H);
-      const int s0 = cached ? s_start[b] : a.plan.block_start[b], s1 = cached ? s_start[b + 1] : a.plan.block_start[b + 1];
-      const int in = i - s0 * a.H;
-      h = in / (s1 - s0);
-      blk = in - h * (s1 - s0);
-      int b2, blk2;
-      return block_of(s0 + blk, b2, blk2);
-    };
-    int total = 0;
-    for (int base = 0; base < items; base += kSchedThreads) {
-      int b, blk, h;
-      long long cost = base + tid < items ? item_of(base + tid, b, blk, h) : 0, tot;
-      const long long incl = block_inclusive_scan(cost, scan_scratch[0], &tot);
-      if (base + tid < items) cum[base + tid] = total + (int)incl;
-      total += (int)tot;
+  if (cached && items <= a.max_cut) {
+    // Most tiles of an item, for each user (s_wave) and in all.
+    if (tid < a.B) s_wave[tid] = 0;
+    __syncthreads();
+    for (int g = tid; g < nblocks; g += kSchedThreads) {
+      int b, blk;
+      const int cost = block_of(g, b, blk);
+      atomicMax(&s_wave[b], cost);
+      atomicMax(&longest, cost);
     }
     __syncthreads();
-    const int most = total / kMinRangeTiles;
-    const int ranges = most < 1 ? 1 : (most < a.num_ctas ? most : a.num_ctas);
-    int pieces = 0;
-    for (int base = 0; base < items; base += kSchedThreads) {
-      const int i = base + tid;
-      int c0 = 0, c1 = 0, r0 = 0, parts = 0;
-      if (i < items) {
-        c0 = i > 0 ? cum[i - 1] : 0;
-        c1 = cum[i];
-        r0 = range_of(total, ranges, c0);
-        parts = range_of(total, ranges, c1 - 1) - r0 + 1;
+    // Pieces when the longest item is cut in c, for c = 1 .. kMaxCuts.
+    const int top = longest;
+    if (tid < a.B) {
+      const int64_t rows = (int64_t)(s_start[tid + 1] - s_start[tid]) * a.H;
+#pragma unroll
+      for (int c = 1; c <= kMaxCuts; ++c) {
+        const int64_t n = rows * cdiv(s_wave[tid], cdiv(top, c));
+        if (n) atomicAdd(&pieces_of[c], (int)(n < a.max_cut + 1 ? n : a.max_cut + 1));
       }
-      long long tot;
-      const int first = pieces + (int)block_inclusive_scan(parts, scan_scratch[0], &tot) - parts;
-      pieces += (int)tot;
-      if (i < items) {
+    }
+    __syncthreads();
+    // The best c by estimated time, ties to the smaller: lane c - 1 of each warp rates c.
+    int best = (tid & 31) + 1, time = INT_MAX;
+    if (best <= kMaxCuts && best <= top && pieces_of[best] <= a.max_cut) {
+      const int q = cdiv(top, best);
+      if (best == 1 || q >= kMinPieceTiles)
+        time = cdiv(pieces_of[best], a.num_ctas) * (q + (best > 1 ? kPieceOverhead : 0));
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      const int t2 = __shfl_xor_sync(0xffffffffu, time, o), b2 = __shfl_xor_sync(0xffffffffu, best, o);
+      if (t2 < time || (t2 == time && b2 < best)) {
+        time = t2;
+        best = b2;
+      }
+    }
+    if (best > 1) {
+      // Queue places: user, head, part, block.  Every item of a user is cut alike; the places of parts
+      // that a short item does not have stay empty.
+      const int q = cdiv(top, best);
+      long long mine = 0, tot;
+      if (tid < a.B) mine = (long long)(s_start[tid + 1] - s_start[tid]) * a.H * cdiv(s_wave[tid], q);
+      const int first = (int)(block_inclusive_scan(mine, scan_scratch[0], &tot) - mine);
+      if (tid < a.B) hist[tid] = first;
+      __syncthreads();
+      for (int x = tid; x < nblocks * a.H; x += kSchedThreads) {
         PagedPiece p;
-        item_of(i, p.b, p.block, p.h);
-        p.parts = parts;
-        p.slot = parts > 1 ? atomicAdd(&slots, parts) : 0;  // any order: a slot only names a place
-        for (int k = 0; k < parts; ++k) {
-          const int lo = max(c0, range_begin(total, ranges, r0 + k));
-          const int hi = r0 + k + 1 < ranges ? min(c1, range_begin(total, ranges, r0 + k + 1)) : c1;
-          p.tile0 = lo - c0;
-          p.tiles = hi - lo;
-          p.part = k;
-          a.plan.pieces[first + k] = p;
-          if (lo == range_begin(total, ranges, r0 + k)) a.plan.starts[r0 + k] = first + k;
+        p.h = x / nblocks;
+        const int cost = block_of(x - p.h * nblocks, p.b, p.block);
+        const int parts = cdiv(s_wave[p.b], q);
+        p.pitch = s_start[p.b + 1] - s_start[p.b];
+        p.parts = min(parts, cost);
+        const int at = hist[p.b] + p.h * parts * p.pitch + p.block;
+        for (p.part = 0; p.part < parts; ++p.part) {
+          p.tile0 = p.part < p.parts ? cost * p.part / p.parts : 0;
+          p.tiles = p.part < p.parts ? cost * (p.part + 1) / p.parts - p.tile0 : 0;
+          a.plan.pieces[at + p.part * p.pitch] = p;
         }
-        if (parts > 1)
-          for (int q = 0; q < 4; ++q) a.plan.done[p.slot * 4 + q] = 0;
+        for (int k = 0; k < 4; ++k) a.plan.done[at * 4 + k] = 0;
       }
+      if (tid == 0) {
+        a.plan.header[0] = 0;
+        a.plan.header[1] = (int)tot;
+        a.plan.header[2] = 0;
+        a.plan.header[3] = best;
+      }
+      return;
     }
+    // Whole items after all: one wave.
+    if (tid < a.B) s_wave[tid] = 0;
     __syncthreads();
-    if (tid == 0) {
-      a.plan.starts[ranges] = pieces;
-      a.plan.header[0] = 0;
-      a.plan.header[1] = pieces;
-      a.plan.header[2] = 0;
-      a.plan.header[3] = items > 0 ? ranges : 0;
-      a.plan.header[4] = slots;
-    }
-    return;
   }
 
-  // -------------------------------------------------------------------- queue
-  // As schedule_kernel: a counting sort of the blocks by (wave, non-increasing cost).
+  // Whole items, as schedule_kernel: a counting sort of the blocks by (wave, non-increasing cost).
   const int nkeys = a.nbins * a.nwaves;
+  for (int i = tid; i < nkeys; i += kSchedThreads) hist[i] = 0;
+  __syncthreads();
   auto key_of = [&](int b, int cost) {
     int wave = 0;
     if (cached) wave = s_wave[b];
@@ -222,10 +216,10 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   for (int g = tid; g < nblocks; g += kSchedThreads) {
     PagedPiece p;
     const int cost = block_of(g, p.b, p.block);
-    p.parts = 1;
     p.tile0 = 0;
     p.tiles = cost;
-    p.slot = p.part = 0;
+    p.parts = 1;
+    p.part = p.pitch = 0;
     const int pos = atomicAdd(&hist[key_of(p.b, cost)], a.H);
     for (p.h = 0; p.h < a.H; ++p.h)
       if (pos + p.h < items) a.plan.pieces[pos + p.h] = p;
@@ -234,8 +228,7 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     a.plan.header[0] = 0;
     a.plan.header[1] = items;
     a.plan.header[2] = 0;
-    a.plan.header[3] = 0;
-    a.plan.header[4] = 0;
+    a.plan.header[3] = 1;
   }
 }
 

@@ -6,6 +6,21 @@ import re
 
 import pytest
 
+class PagedCache(ctypes.Structure):
+    """hstu_paged_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int32),
+                ("table_ld", ctypes.c_int64)]
+
+
+class Rotation(ctypes.Structure):
+    """hstu_rotation_t."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("pairs", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("positions_ld", ctypes.c_int64)]
+
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "hstu_paged.h")
 OK, INVALID, UNSUPPORTED = 0, 1, 2
@@ -30,22 +45,33 @@ def test_exports(lib):
         assert re.search(r"\sT %s$" % name, out, re.M), name
 
 
-def _rotation(**kw):
+def test_packed_structs():
+    """The binding packs the two structs as bytes; the layout is the C compiler's."""
     from hstu_pointwise_attention_jagged_b200 import paged
+    raw = paged._CACHE.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
+    c = PagedCache.from_buffer_copy(raw)
+    assert len(raw) == ctypes.sizeof(PagedCache)
+    assert [getattr(c, n) for n, _ in PagedCache._fields_] == list(range(1, 11))
+    raw = paged._ROTATION.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
+    r = Rotation.from_buffer_copy(raw)
+    assert len(raw) == ctypes.sizeof(Rotation)
+    assert [r.freqs, r.pairs, r.axes, *r.sections, r.interleaved, r.positions, r.positions_ld] == list(range(1, 11))
+
+
+def _rotation(**kw):
     a = dict(freqs=1 << 12, pairs=32, axes=1, interleaved=0, positions=1 << 13, positions_ld=0)
     sections = kw.pop("sections", [32])
     a.update(kw)
-    r = paged.Rotation(**a)
+    r = Rotation(**a)
     r.sections[:len(sections)] = sections
     return r
 
 
 def _cache(**kw):
-    from hstu_pointwise_attention_jagged_b200 import paged
     a = dict(k=1 << 30, v=1 << 31, page_stride=16 * 128, row_stride=128, head_stride=64, num_pages=8, page_size=16,
              page_table=1 << 12, table_width=4, table_ld=4)
     a.update(kw)
-    return paged.PagedCache(**a)
+    return PagedCache(**a)
 
 
 def _rotary(lib, rot=None, **kw):
