@@ -138,45 +138,82 @@ hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState
   return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
-// CTAs that share one (user, head, row block) in the few-rows kernel.
-int rows_split(int64_t clusters, int64_t tiles, int num_sms) {
-  int s = 1;
-  while (s < kRowsMaxSplit && clusters * s < 4 * static_cast<int64_t>(num_sms) && s < tiles) s *= 2;
-  return s;
-}
-
-template <int D>
-hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t stream) {
-  static std::once_flag once[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return HSTU_ERR_CUDA;
-  cudaError_t e = cudaSuccess;
-  std::call_once(once[dev], [&] {
-    e = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::kSmemBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  if (e != cudaSuccess) return HSTU_ERR_CUDA;
-  const int64_t clusters = static_cast<int64_t>(a.B) * a.H * a.blocks;
-  const int64_t tiles = (a.max_kv + RowsCfg<D>::kKeys - 1) / RowsCfg<D>::kKeys;
-  int S = rows_split(clusters, tiles, st.num_sms);
-  if (clusters * S > INT_MAX) return HSTU_ERR_UNSUPPORTED;
+// Programmatic dependents of the previous kernel in the stream: a launch's set-up overlaps that kernel's
+// tail, and the kernel waits for it (griddepcontrol.wait) before touching global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int threads, int smem, int cluster,
+                             cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * S));
-  cfg.blockDim = dim3(kRowsThreads);
-  cfg.dynamicSmemBytes = RowsCfg<D>::kSmemBytes;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D>, a) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Sets a kernel up once for each device.
+constexpr int kMaxDevices = 64;
+
+template <typename F>
+cudaError_t once_per_device(std::once_flag (&once)[kMaxDevices], cudaError_t (&result)[kMaxDevices], F&& f) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] { result[dev] = f(); });
+  return result[dev];
+}
+
+// At most 16 rows a user.
+template <int D>
+hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t stream) {
+  using Cfg = RowsCfg<D>;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t ready[kMaxDevices];
+  cudaError_t e = once_per_device(once, ready, [] {
+    cudaError_t r = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(paged_rows_run_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    return r;
+  });
+  if (e != cudaSuccess) return HSTU_ERR_CUDA;
+  const int64_t items = static_cast<int64_t>(a.B) * a.H;
+  const int64_t tiles = a.max_kv / Cfg::kKeys + 1;  // of an item, at most
+  // Clusters as large as keeps every CTA resident at once and busy with two tiles, if that leaves each CTA a
+  // short stretch of tiles: then one launch does it all.  A long stretch takes the equal runs, which ragged
+  // lengths cannot unbalance.  (us, d = 128, one row a user: 64 users x 4 heads of 700 rows, 11 tiles a CTA,
+  // 18.2 against 24.0; 16 x 4 of 3000, 12 tiles, 20.3 against 24.2; 64 x 4 of ragged histories up to 4096,
+  // 64 tiles, 62 against 41; 1 x 4 of 32000, 31 tiles, 29 against 20.)
+  int cluster = 1;
+  while (cluster < kRowsMaxSplit && 2 * cluster * items <= 2 * st.num_sms && 4 * cluster <= tiles) cluster *= 2;
+  if ((tiles + cluster - 1) / cluster <= kRowsClusterTiles || a.B > kRunUsers || items * tiles > INT_MAX) {
+    if (items * cluster > INT_MAX) return HSTU_ERR_UNSUPPORTED;
+    e = launch_dependent(paged_rows_kernel<D>, items * cluster, kRowsThreads, Cfg::kSmemBytes, cluster, stream, a);
+    return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  }
+  const int runs = 2 * st.num_sms;
+  const size_t parts_bytes = (static_cast<size_t>(items) * sizeof(int2) + 255) / 256 * 256;
+  void* buf = nullptr;
+  if (cudaMallocFromPoolAsync(&buf, parts_bytes + static_cast<size_t>(2 * runs) * kRowsBlock * D * 4, st.pool, stream) !=
+      cudaSuccess)
+    return HSTU_ERR_CUDA;
+  RunsArgs r;
+  r.rows = a;
+  r.parts = static_cast<int2*>(buf);
+  r.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + parts_bytes);
+  e = launch_dependent(paged_rows_run_kernel<D>, runs, kRowsThreads, Cfg::kSmemBytes, 0, stream, r);
+  if (e == cudaSuccess) e = launch_dependent(paged_rows_sum_kernel<D>, items, kSumThreads, 0, 0, stream, r);
+  if (cudaFreeAsync(buf, stream) != cudaSuccess && e == cudaSuccess) return HSTU_ERR_CUDA;
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
@@ -207,36 +244,17 @@ bool encode_q(CUtensorMap* map, const void* base, int64_t rows, int64_t width, i
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
-                             const Args&... args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Many rows a user: the plan, then the tcgen05 kernel, over one buffer from the library's pool.
 template <int D>
 hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, float alpha, DeviceState& st,
                           cudaStream_t stream) {
-  static std::once_flag once[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64 || !tensor_map_encoder()) return HSTU_ERR_CUDA;
-  cudaError_t e = cudaSuccess;
-  std::call_once(once[dev], [&] {
-    e = cudaFuncSetAttribute(hstu_fwd_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             FwdCfg<D>::kSmemBytes);
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t ready[kMaxDevices];
+  cudaError_t e = once_per_device(once, ready, [] {
+    return cudaFuncSetAttribute(hstu_fwd_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                FwdCfg<D>::kSmemBytes);
   });
-  if (e != cudaSuccess) return HSTU_ERR_CUDA;
+  if (e != cudaSuccess || !tensor_map_encoder()) return HSTU_ERR_CUDA;
   const int ctas = st.num_sms;
   const int64_t capacity = static_cast<int64_t>(a.H) * (a.total_new / kItemRows + a.B);
   if (capacity > INT_MAX / 2) return HSTU_ERR_UNSUPPORTED;
@@ -293,9 +311,9 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   p.paged.kv_len = a.kv_len;
   p.paged.plan = s.plan;
   p.paged.partials = reinterpret_cast<float4*>(at + o_partials);
-  e = launch_dependent(paged_schedule_kernel, 1, kSchedThreads, 0, stream, s);
+  e = launch_dependent(paged_schedule_kernel, 1, kSchedThreads, 0, 0, stream, s);
   if (e == cudaSuccess)
-    e = launch_dependent(hstu_fwd_kernel<D, false, true>, ctas, kNumThreads, FwdCfg<D>::kSmemBytes, stream, tq, tk, tv, p);
+    e = launch_dependent(hstu_fwd_kernel<D, false, true>, ctas, kNumThreads, FwdCfg<D>::kSmemBytes, 0, stream, tq, tk, tv, p);
   if (cudaFreeAsync(buf, stream) != cudaSuccess && e == cudaSuccess) return HSTU_ERR_CUDA;
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
@@ -417,8 +435,6 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
   a.num_targets = num_targets;
   a.B = B;
   a.H = H;
-  const int32_t most = max_new < total_new ? max_new : total_new;
-  a.blocks = most > kRowsBlock ? (most + kRowsBlock - 1) / kRowsBlock : 1;
   a.total_new = total_new;
   a.max_new = max_new;
   a.max_kv = max_kv;
@@ -426,7 +442,7 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
   a.inv_n = 1.0f / N;
   a.err = st->err_word;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (most > kRowsBlock)
+  if ((max_new < total_new ? max_new : total_new) > kRowsBlock)
     return d == 128 ? launch_many<128>(a, *cache, alpha, *st, cs)
                     : (d == 64 ? launch_many<64>(a, *cache, alpha, *st, cs) : launch_many<32>(a, *cache, alpha, *st, cs));
   return d == 128 ? launch_rows<128>(a, *st, cs) : (d == 64 ? launch_rows<64>(a, *st, cs) : launch_rows<32>(a, *st, cs));

@@ -81,6 +81,7 @@ def test_few_rows(case, d):
     users, page, H, layout = SMALL[case]
     x = Batch(users, page, H, d, layout, seed=case + 1)
     x.check(x.run())
+    x.check(x.run(max_kv=200000))  # a bound that makes it equal runs of tiles
     assert binding.hstu_attn_get_error() == 0
 
 
@@ -91,6 +92,20 @@ def test_many_rows(case, d):
     x = Batch(users, page, H, d, layout, seed=case + 11)
     x.check(x.run())
     assert binding.hstu_attn_get_error() == 0
+
+
+@pytest.mark.parametrize("users", [300, 1024, 1025, 5000])
+def test_many_users_of_few_rows(users):
+    """Ragged histories, some users without new rows, over the sizes at which the kernel's form changes."""
+    rng = np.random.default_rng(users)
+    new = rng.integers(0, 3, users)
+    cached = np.minimum((30 * rng.lognormal(0, 1.5, users)).astype(int), 700)
+    x = Batch([(int(c), int(n), int(rng.integers(0, n + 1))) for c, n in zip(cached, new)], 16, 1, 32, seed=users)
+    x.check(x.run(), only=set(rng.choice(users, 200).tolist()) | {0, users - 1})
+    assert binding.hstu_attn_get_error() == 0
+    big = [(int(c), int(n), 0) for c, n in zip(cached, 20 * new)]  # the same through the many-row kernel
+    x = Batch(big, 16, 1, 32, seed=users + 1)
+    x.check(x.run(), only=set(rng.choice(users, 200).tolist()) | {0, users - 1})
 
 
 @pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256, 512, 1024])
