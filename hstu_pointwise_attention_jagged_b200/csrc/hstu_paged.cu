@@ -123,21 +123,6 @@ void set_rotation(RotArgs& a, const hstu_rotation_t* r, bool inverse) {
   a.sign = inverse ? -1.0f : 1.0f;
 }
 
-// Rows of a block: about four batches' worth of units for its threads, fewer where that would leave
-// SMs without a block (a call for a few rows is bound by the latency of one block).
-hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState& st, cudaStream_t stream) {
-  a.head_shift = d == 128 ? 3 : (d == 64 ? 2 : 1);
-  const int64_t row_units = static_cast<int64_t>(a.tensors) * a.H << a.head_shift;
-  int64_t r = kRotThreads * kRotBatch / row_units;
-  const int64_t spread = a.rows / (2 * st.num_sms);
-  r = r < spread ? r : spread;
-  a.rows_per_block = static_cast<int32_t>(r < 1 ? 1 : (r > kRotMaxRows ? kRotMaxRows : r));
-  const int grid = (a.rows + a.rows_per_block - 1) / a.rows_per_block;
-  if (paged) rotary_kernel<true><<<grid, kRotThreads, 0, stream>>>(a);
-  else rotary_kernel<false><<<grid, kRotThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
-}
-
 // Programmatic dependents of the previous kernel in the stream: a launch's set-up overlaps that kernel's
 // tail, and the kernel waits for it (griddepcontrol.wait) before touching global memory.
 template <typename... Params, typename... Args>
@@ -159,6 +144,28 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int thread
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Shape of the rotation's blocks: as many rows side by side as have a thread for each unit, a batch of
+// units for each thread; fewer rows where that would leave SMs without a block (a call for a few rows is
+// bound by the latency of one block).
+hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState& st, cudaStream_t stream) {
+  a.head_shift = d == 128 ? 3 : (d == 64 ? 2 : 1);
+  const int64_t units = static_cast<int64_t>(a.tensors) * a.H << a.head_shift;
+  if (units > INT_MAX / 2) return HSTU_ERR_UNSUPPORTED;
+  const int spread = a.rows / (2 * st.num_sms) > 1 ? a.rows / (2 * st.num_sms) : 1;
+  auto at_most = [](int64_t x, int64_t y) { return static_cast<int32_t>(x < y ? x : y); };
+  a.row_units = static_cast<int32_t>(units);
+  a.side_rows = units < kRotThreads ? at_most(kRotThreads / units, kRotMaxRows / kRotBatch) : 1;
+  a.side_rows = at_most(a.side_rows, spread);
+  a.block_rows = at_most(a.side_rows * kRotBatch, spread);
+  int threads = at_most((a.side_rows * units + 31) / 32 * 32, kRotThreads);
+  if (threads < 64) threads = 64;  // the angles: at least one thread a pair
+  const int grid = (a.rows + a.block_rows - 1) / a.block_rows;
+  const int smem = a.block_rows * a.pairs * 8;
+  const cudaError_t e = paged ? launch_dependent(rotary_kernel<true>, grid, threads, smem, 0, stream, a)
+                              : launch_dependent(rotary_kernel<false>, grid, threads, smem, 0, stream, a);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
 // Sets a kernel up once for each device.

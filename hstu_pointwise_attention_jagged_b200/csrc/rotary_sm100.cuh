@@ -2,14 +2,16 @@
 // or, for K and V, to their places in a paged cache (hstu_paged_append).
 //
 // A pair (x, y) of a head turns by t = pos * freq: (x cos t - y sin t, x sin t + y cos t).  One
-// cos/sin pair serves every head of Q and of K, so a block of R rows first forms its R x pairs table
+// cos/sin pair serves every head of Q and of K, so a block of rows first forms its rows x pairs table
 // in shared memory and then streams its rows through it.  What bounds the kernel is the rows' bytes, read
-// and written once (4 bytes an element): the first batch of 32-byte units is loaded before the
-// table is formed, so the row traffic covers the angles' arithmetic.
+// and written once (4 bytes an element), if the instructions for a 32-byte unit stay few: a thread
+// keeps one place within the row (tensor, head, columns), decoded once, and steps through rows.  Its
+// first units are loaded before the table is formed, so their latency covers the angles' arithmetic
+// and the look-ups in offsets and page table.
 //
-// Angles.  pos is up to 2^31 (Unix times), where pos * freq in fp32 has no correct digit left.  The
-// angle is formed in turns, pos * (freq / 2 pi), in fp64; only its fraction, exact to 2^-53 of the
-// whole, is rounded to fp32 and goes to sincospif.
+// Angles.  pos is up to 2^31 (Unix times), where pos * freq in fp32 has no correct digit left.  They are
+// formed in turns, in 64-bit fixed point: freq / 2 pi modulo one turn is a whole number of 2^-64 turns,
+// its product with pos wraps modulo one turn by itself, and the upper half of it goes to sincospif.
 #pragma once
 
 #include <climits>
@@ -21,9 +23,9 @@
 
 namespace hstu {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 256;    // at most
 constexpr int kRotBatch = 4;        // 32-byte units a thread has in flight
-constexpr int kRotMaxRows = 16;     // rows of a block
+constexpr int kRotMaxRows = 64;     // rows of a block
 constexpr int kRotMaxPairs = 64;
 constexpr int kRotScanUsers = 1024; // batches up to this size: each block scans the offsets for its rows' users
 
@@ -40,8 +42,12 @@ struct RotTensor {
 
 struct RotArgs {
   RotTensor t[3];
-  int32_t tensors, rows, rows_per_block, H;
+  int32_t tensors, rows, H;
   int32_t head_shift;   // log2(d / 16): 32-byte units of a head
+  // A block takes `block_rows` rows, `side_rows` of them side by side: thread x has place x % row_units of
+  // rows x / row_units + k * side_rows (one row at a time, several places, when a row has more units than
+  // the block has threads).
+  int32_t row_units, side_rows, block_rows;
   // rotation; pairs = 0 for plain copies
   const double* freqs;
   const int32_t* positions;  // null: the row's place in the cache
@@ -90,152 +96,175 @@ __device__ __forceinline__ void turn_unit(RotUnit& u, const float4 (&cs)[4], boo
   u.b = make_uint4(wb[0], wb[1], wb[2], wb[3]);
 }
 
+// freq (radians) as 2^-64 turns, modulo one turn.
+__device__ __forceinline__ uint64_t turns_of(double freq) {
+  const double t = freq * 0.15915494309189533577;  // 1 / 2 pi
+  return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
+}
+
 template <bool kPaged>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs p) {
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotArgs p) {
   // (cos, sin) of row r, pair 8 u + 2 j + e at float2 index ((r * 4 + j) * (pairs / 8) + u) * 2 + e, so
   // that neighbouring units read neighbouring float4.
-  __shared__ float4 s_cs[kRotMaxRows * kRotMaxPairs / 2];
-  __shared__ int64_t s_dst[kRotMaxRows];  // element offset of the row in the cache, -1: not written
-  __shared__ int32_t s_place[kRotMaxRows], s_user[kRotMaxRows];
-  const int tid = threadIdx.x;
-  const int row0 = blockIdx.x * p.rows_per_block;
-  const int nrows = min(p.rows_per_block, p.rows - row0);
+  extern __shared__ float4 s_cs[];
+  __shared__ int64_t s_dst[kRotMaxRows];            // element offset of the row in the cache, -1: not written
+  __shared__ unsigned long long s_key[kRotMaxRows]; // user << 32 | place of the row, ~0: no user's row
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int row0 = blockIdx.x * p.block_rows;
+  const int nrows = min(p.block_rows, p.rows - row0);
   const int pairs = p.pairs;
-  const uint32_t head_units = 1u << p.head_shift;
-  const uint32_t units = (uint32_t)nrows * p.tensors * p.H * head_units;
+  const int per_pass = p.side_rows * p.row_units;  // threads that take part
 
-  // Unit x of the block: its row, tensor and the columns of its two vectors.
+  // Unit place x of a row: its tensor and the columns of its two vectors.
   struct Place {
-    int r, t;
-    int c0, c1;
+    int t, h, c0, c1, part;  // c0, c1: within the head
     bool turn;
-    int part;
   };
-  auto place_of = [&](uint32_t x) {
+  auto place_of = [&](int x) {
     Place u;
-    u.part = (int)(x & (head_units - 1));
-    const uint32_t y = x >> p.head_shift;
-    const uint32_t rt = y / (uint32_t)p.H;
-    const int h = (int)(y - rt * p.H);
-    u.r = (int)(rt / (uint32_t)p.tensors);
-    u.t = (int)(rt - (uint32_t)u.r * p.tensors);
+    u.part = x & ((1 << p.head_shift) - 1);
+    const int y = x >> p.head_shift;
+    u.t = y / p.H;
+    u.h = y - u.t * p.H;
     u.turn = p.t[u.t].rotated && u.part * 8 < pairs;
-    const int head0 = h << (p.head_shift + 4);
     const bool split = u.turn && !p.interleaved;
-    u.c0 = head0 + (split ? u.part * 8 : u.part * 16);
+    u.c0 = split ? u.part * 8 : u.part * 16;
     u.c1 = split ? u.c0 + pairs : u.c0 + 8;
     return u;
   };
+  const int side = tid / p.row_units;  // 0 when a row has more units than the block has threads
   RotUnit held[kRotBatch];
-  auto load_batch = [&](uint32_t x0) {
+  const __nv_bfloat16* src = nullptr;
+  int64_t src_step = 0;
+  auto aim = [&](const Place& u) {
+    const RotTensor& t = p.t[u.t];
+    src = t.src + (int64_t)(row0 + side) * t.src_ld + (u.h << (p.head_shift + 4));
+    src_step = p.side_rows * t.src_ld;
+  };
+  auto load_batch = [&](const Place& u, int r) {
+    const __nv_bfloat16* from = src;
 #pragma unroll
     for (int i = 0; i < kRotBatch; ++i) {
-      const uint32_t x = x0 + i * kRotThreads;
-      if (x < units) {
-        const Place u = place_of(x);
-        const __nv_bfloat16* src = p.t[u.t].src + (int64_t)(row0 + u.r) * p.t[u.t].src_ld;
-        held[i].a = __ldcs(reinterpret_cast<const uint4*>(src + u.c0));
-        held[i].b = __ldcs(reinterpret_cast<const uint4*>(src + u.c1));
+      if (r + i * p.side_rows < nrows) {
+        held[i].a = __ldcs(reinterpret_cast<const uint4*>(from + u.c0));
+        held[i].b = __ldcs(reinterpret_cast<const uint4*>(from + u.c1));
       }
+      from += src_step;
     }
+    src = from;
   };
-  load_batch(tid);
+  const bool active = tid < per_pass || per_pass > threads;
+  int x = side == 0 ? tid : tid - side * p.row_units;
+  Place u = place_of(x < p.row_units ? x : 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (active) {
+    aim(u);
+    load_batch(u, side);
+  }
 
   if constexpr (kPaged) {
     // Whose rows these are.  Up to kRotScanUsers users every block looks at all offsets, which costs one
     // round of coalesced loads; beyond that each row searches for itself.
-    if (tid < kRotMaxRows) s_user[tid] = INT_MAX;
+    auto claim = [&](int b, int lo, int hi) {
+      const PagedUser v = paged_user(p.cache, p.q_offsets, p.kv_len, nullptr, b, p.rows, INT_MAX, -1);
+      if (!v.ok) return;
+      for (int r = lo; r < hi; ++r)
+        atomicMin(&s_key[r], (unsigned long long)(unsigned)b << 32 | (unsigned)(v.L - v.n + (row0 + r - v.q0)));
+    };
+    if (tid < nrows) s_key[tid] = ~0ull;
     __syncthreads();
     if (p.B <= kRotScanUsers) {
-      for (int b = tid; b < p.B; b += kRotThreads) {
-        const int o0 = p.q_offsets[b], o1 = p.q_offsets[b + 1];
-        const int hi = min(o1, row0 + nrows);
-        for (int r = max(o0, row0); r < hi; ++r) atomicMin(&s_user[r - row0], b);
+      for (int b = tid; b < p.B; b += threads) {
+        const int lo = max(p.q_offsets[b] - row0, 0), hi = min(p.q_offsets[b + 1] - row0, nrows);
+        if (lo < hi) claim(b, lo, hi);
       }
-    } else if (tid < nrows) {
-      int lo = 0, hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (p.q_offsets[mid] <= row0 + tid) lo = mid; else hi = mid;
+    } else {
+      for (int r = tid; r < nrows; r += threads) {
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+          const int mid = lo + (hi - lo) / 2;
+          if (p.q_offsets[mid] <= row0 + r) lo = mid; else hi = mid;
+        }
+        if (p.q_offsets[lo] <= row0 + r && row0 + r < p.q_offsets[lo + 1]) claim(lo, r, r + 1);
       }
-      if (p.q_offsets[lo] <= row0 + tid && row0 + tid < p.q_offsets[lo + 1]) s_user[tid] = lo;
     }
     if (blockIdx.x == 0) {
       bool bad = tid == 0 && (p.q_offsets[0] != 0 || p.q_offsets[p.B] != p.rows);
-      for (int b = tid; b < p.B; b += kRotThreads)
+      for (int b = tid; b < p.B; b += threads)
         bad |= !paged_user(p.cache, p.q_offsets, p.kv_len, nullptr, b, p.rows, INT_MAX, -1).ok;
       if (bad) atomicOr(p.err, kErrBadOffsets);
     }
     __syncthreads();
-    if (tid < nrows) {
+    for (int r = tid; r < nrows; r += threads) {
       int64_t dst = -1;
-      int place = -1;
-      const int b = s_user[tid];
-      if (b != INT_MAX) {
-        const PagedUser u = paged_user(p.cache, p.q_offsets, p.kv_len, nullptr, b, p.rows, INT_MAX, -1);
-        if (u.ok) {
-          place = u.L - u.n + (row0 + tid - u.q0);
-          const int page = p.cache.table[b * p.cache.table_ld + (place >> p.cache.page_shift)];
-          if (page >= 0 && page < p.cache.num_pages)
-            dst = page * p.cache.page_stride + (place & ((1 << p.cache.page_shift) - 1)) * p.cache.row_stride;
-          else
-            atomicOr(p.err, kErrBadOffsets);
-        }
+      if (s_key[r] != ~0ull) {
+        const int b = (int)(s_key[r] >> 32), place = (int)(s_key[r] & 0xffffffffu);
+        const int page = p.cache.table[b * p.cache.table_ld + (place >> p.cache.page_shift)];
+        if (page >= 0 && page < p.cache.num_pages)
+          dst = page * p.cache.page_stride + (place & ((1 << p.cache.page_shift) - 1)) * p.cache.row_stride;
+        else
+          atomicOr(p.err, kErrBadOffsets);
       }
-      s_dst[tid] = dst;
-      s_place[tid] = place;
+      s_dst[r] = dst;
     }
-    __syncthreads();
   }
 
-  for (int x = tid; x < nrows * pairs; x += kRotThreads) {
-    const int r = x / pairs, i = x - r * pairs;
-    const int axis = (p.axes > 1 && i >= p.section_end[0]) + (p.axes > 2 && i >= p.section_end[1]) +
-                     (p.axes > 3 && i >= p.section_end[2]);
-    int pos;
-    if (kPaged && p.positions == nullptr) pos = s_place[r];
-    else pos = p.positions[axis * p.positions_ld + row0 + r];
-    constexpr double kInv2Pi = 0.15915494309189533577;
-    const double turns = pos * (p.freqs[i] * kInv2Pi);
-    float sn, cs;
-    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-    reinterpret_cast<float2*>(s_cs)[((r * 4 + ((i >> 1) & 3)) * (pairs >> 3) + (i >> 3)) * 2 + (i & 1)] =
-        make_float2(cs, p.sign * sn);
+  if (pairs > 0) {
+    // Thread -> pair tid % pairs of rows tid / pairs + k * (threads / pairs).
+    const int i = tid % pairs, step = threads / pairs;
+    if (tid < step * pairs) {
+      const int axis = (p.axes > 1 && i >= p.section_end[0]) + (p.axes > 2 && i >= p.section_end[1]) +
+                       (p.axes > 3 && i >= p.section_end[2]);
+      const uint64_t turns = turns_of(p.freqs[i]);
+      const int32_t* pos = p.positions ? p.positions + axis * p.positions_ld + row0 : nullptr;
+      float2* to = reinterpret_cast<float2*>(s_cs) + (((i >> 1) & 3) * (pairs >> 3) + (i >> 3)) * 2 + (i & 1);
+      for (int r = tid / pairs; r < nrows; r += step) {
+        const int at = pos ? pos[r] : (int)(s_key[r] & 0xffffffffu);
+        const int part = (int)(uint32_t)(((uint64_t)(int64_t)at * turns) >> 32);  // 2^-32 turns, signed
+        float sn, cs;
+        sincospif((float)part * 0x1p-31f, &sn, &cs);
+        to[r * pairs] = make_float2(cs, p.sign * sn);
+      }
+    }
   }
   __syncthreads();
+  if (!active) return;
 
-  const int64_t cache_head = p.cache.head_stride;
-  for (uint32_t x0 = tid; x0 < units; x0 += kRotBatch * kRotThreads) {
-    if (x0 != (uint32_t)tid) load_batch(x0);
+  while (true) {
+    const RotTensor& t = p.t[u.t];
+    const bool cached = kPaged && t.target != kToRows;
+    __nv_bfloat16* base = cached ? (t.target == kToCacheK ? p.cache.k : p.cache.v) + u.h * p.cache.head_stride
+                                 : t.dst + (int64_t)row0 * t.dst_ld + (u.h << (p.head_shift + 4));
+    for (int r0 = side; r0 < nrows; r0 += kRotBatch * p.side_rows) {
+      if (r0 != side) load_batch(u, r0);
 #pragma unroll
-    for (int i = 0; i < kRotBatch; ++i) {
-      const uint32_t x = x0 + i * kRotThreads;
-      if (x >= units) break;
-      const Place u = place_of(x);
-      if (u.turn) {
-        float4 cs[4];
+      for (int i = 0; i < kRotBatch; ++i) {
+        const int r = r0 + i * p.side_rows;
+        if (r >= nrows) break;
+        if (u.turn) {
+          float4 cs[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) cs[j] = s_cs[(u.r * 4 + j) * (pairs >> 3) + u.part];
-        turn_unit(held[i], cs, p.interleaved);
+          for (int j = 0; j < 4; ++j) cs[j] = s_cs[(r * 4 + j) * (pairs >> 3) + u.part];
+          turn_unit(held[i], cs, p.interleaved);
+        }
+        int64_t to;
+        if (cached) {
+          to = s_dst[r];
+          if (to < 0) continue;
+        } else {
+          if (kPaged && s_key[r] == ~0ull) continue;
+          to = r * t.dst_ld;
+        }
+        *reinterpret_cast<uint4*>(base + to + u.c0) = held[i].a;
+        *reinterpret_cast<uint4*>(base + to + u.c1) = held[i].b;
       }
-      const RotTensor& t = p.t[u.t];
-      __nv_bfloat16 *d0, *d1;
-      if (kPaged && t.target != kToRows) {
-        if (s_dst[u.r] < 0) continue;
-        const int d_mask = (16 << p.head_shift) - 1;
-        __nv_bfloat16* base = (t.target == kToCacheK ? p.cache.k : p.cache.v) + s_dst[u.r] +
-                              (u.c0 >> (p.head_shift + 4)) * cache_head;
-        d0 = base + (u.c0 & d_mask);
-        d1 = base + (u.c1 & d_mask);
-      } else {
-        if (kPaged && s_place[u.r] < 0) continue;
-        __nv_bfloat16* base = t.dst + (int64_t)(row0 + u.r) * t.dst_ld;
-        d0 = base + u.c0;
-        d1 = base + u.c1;
-      }
-      *reinterpret_cast<uint4*>(d0) = held[i].a;
-      *reinterpret_cast<uint4*>(d1) = held[i].b;
     }
+    x += threads;
+    if (per_pass <= threads || x >= p.row_units) break;
+    u = place_of(x);
+    aim(u);
+    load_batch(u, side);
   }
 }
 

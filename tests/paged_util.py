@@ -26,10 +26,11 @@ def rotate64(x, positions, freqs, sections, interleaved=False, inverse=False):
 
 def rotation_bound(x, want, pairs, interleaved):
     """Largest error a correct rotation makes, element by element.  The value is rounded to bf16 once
-    (half a step: 2^-8 of it).  Before that, times the pair's |x| + |y|: the angle in fp64 turns is off by
-    three roundings of 2^-53 of at most 2^28.4 turns (positions below 2^31, frequencies up to 1),
-    7.8e-7 radians; its fraction rounded to fp32 by 2^-25 turns, 1.9e-7; sincospif by two steps, 1.2e-7;
-    and three fp32 operations by 2^-24 each, 1.8e-7: 1.3e-6 < 2^-19.5 in all."""
+    (half a step: 2^-8 of it).  Before that, times the pair's |x| + |y|: the angle in turns carries the two
+    fp64 roundings of freq / 2 pi, 2^-53 each of at most 2^28.4 turns (positions below 2^31,
+    frequencies up to 1), 5.2e-7 radians, and the 2^-32 turns cut off below its upper half, 1.5e-9; rounded to
+    fp32 it is off by another 2^-25 turns, 1.9e-7; sincospif by two steps, 1.2e-7; and three fp32
+    operations by 2^-24 each, 1.8e-7: 1.02e-6 < 2^-19.5 in all."""
     x = np.abs(np.asarray(x, np.float64))
     s = np.zeros_like(x)
     for i in range(pairs):
