@@ -146,8 +146,8 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int thread
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Shape of the rotation's blocks: as many rows side by side as have a thread for each unit, a batch of
-// units for each thread; fewer rows where that would leave SMs without a block (a call for a few rows is
+// Shape of the rotation's blocks: as many rows side by side as have a thread for each unit, and
+// kRotBatch x kRotPasses units for each thread; fewer rows where that would leave SMs without a block (a call for a few rows is
 // bound by the latency of one block).
 hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState& st, cudaStream_t stream) {
   a.head_shift = d == 128 ? 3 : (d == 64 ? 2 : 1);
@@ -156,9 +156,9 @@ hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState
   const int spread = a.rows / (2 * st.num_sms) > 1 ? a.rows / (2 * st.num_sms) : 1;
   auto at_most = [](int64_t x, int64_t y) { return static_cast<int32_t>(x < y ? x : y); };
   a.row_units = static_cast<int32_t>(units);
-  a.side_rows = units < kRotThreads ? at_most(kRotThreads / units, kRotMaxRows / kRotBatch) : 1;
+  a.side_rows = units < kRotThreads ? at_most(kRotThreads / units, kRotSideRows) : 1;
   a.side_rows = at_most(a.side_rows, spread);
-  a.block_rows = at_most(a.side_rows * kRotBatch, spread);
+  a.block_rows = at_most(a.side_rows * kRotBatch * kRotPasses, spread);
   int threads = at_most((a.side_rows * units + 31) / 32 * 32, kRotThreads);
   if (threads < 64) threads = 64;  // the angles: at least one thread a pair
   const int grid = (a.rows + a.block_rows - 1) / a.block_rows;

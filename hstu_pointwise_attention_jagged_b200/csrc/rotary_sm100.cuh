@@ -24,8 +24,11 @@
 namespace hstu {
 
 constexpr int kRotThreads = 256;    // at most
-constexpr int kRotBatch = 4;        // 32-byte units a thread has in flight
-constexpr int kRotMaxRows = 64;     // rows of a block
+// Units a thread has in flight, and how often over (measured at 2 x 2, 4 x 1, 4 x 2, 2 x 1 and 1 x 4: rotation of
+// 32768 x 512 Q and K in 23.6, 25.5, 25.6, 26.2 and 26.7 us, streaming append 45.7, 49.3, 47.0, 54.6 and 45.8).
+constexpr int kRotBatch = 2, kRotPasses = 2;
+constexpr int kRotSideRows = 16;    // rows side by side at most
+constexpr int kRotMaxRows = kRotSideRows * kRotBatch * kRotPasses;  // rows of a block
 constexpr int kRotMaxPairs = 64;
 constexpr int kRotScanUsers = 1024; // batches up to this size: each block scans the offsets for its rows' users
 
@@ -103,7 +106,7 @@ __device__ __forceinline__ uint64_t turns_of(double freq) {
 }
 
 template <bool kPaged>
-__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotArgs p) {
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotArgs p) {
   // (cos, sin) of row r, pair 8 u + 2 j + e at float2 index ((r * 4 + j) * (pairs / 8) + u) * 2 + e, so
   // that neighbouring units read neighbouring float4.
   extern __shared__ float4 s_cs[];
