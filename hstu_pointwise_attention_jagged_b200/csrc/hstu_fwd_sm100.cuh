@@ -89,6 +89,9 @@ constexpr int kNumThreads = 448;  // 8 SiLU warps + producer + MMA issuer + 4 ep
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;       // issues every MMA and owns the TMEM allocation
 constexpr int kEpiWarp0 = 10;     // first of the four epilogue warps
+constexpr int kPagedProducers = 3;  // producer warps of the paged form: kProducerWarp and those from
+constexpr int kPagedWarp0 = 14;     // kPagedWarp0 on (512 threads of 128 registers fill the register file)
+constexpr int kPagedThreads = kNumThreads + 32 * (kPagedProducers - 1);
 constexpr int kSlots = 4;         // work-item slots between the producer and the other roles
 constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s per wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;  // 0.2 s per drain wait on the abort path
@@ -131,8 +134,8 @@ struct SmemCtl {
   uint64_t drain;
   uint64_t v_tail;  // paged form: a V tile whose last rows are still to be cleared
   // work slot: valid, h, kv_start, q_row0, pos0, nrows, L, U; paged form: tile0, tiles, parts, part,
-  // pitch too, and the queue place of the item's first part in place of kv_start
-  int32_t slot[kSlots][13];
+  // pitch, user too, and the queue place of the item's first part in place of kv_start
+  int32_t slot[kSlots][14];
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -323,18 +326,24 @@ __device__ __forceinline__ void silu_tile(uint32_t taddr_s, float half_alpha, in
 // whole ring.)
 __device__ __forceinline__ int group_of_load(int e) { return e < 3 ? e : (e + 3) >> 1; }
 
-// Producer of the paged form, run by the whole warp: the pages of a key tile are copied by as many lanes,
-// one each, whose table entries were read one tile ahead.  The order of the loads and the barriers are
-// the contiguous producer's (see the kernel below).
+// Producers of the paged form: kPagedProducers warps, of which `who` = 0 takes the pieces from the queue
+// and does all that the contiguous producer does (see the kernel below), in the same order; the others
+// follow it through the work slots.  They share out the copies: a key tile is one copy for each of its pages
+// and column blocks, at most 32, and lane o of every warp holds copy o's table entry, read a tile
+// ahead, and issues it if o mod kPagedProducers is the warp's number.  A warp spends about 60 cycles on a
+// copy, and the 32 copies a group of 16-row pages needs at d = 128 would take one warp twice the time of
+// the group's arithmetic.  A copy may complete on a group's barrier before the first warp has announced its
+// bytes there: the phase stays open for that warp's arrival.
 //
 // A page the user does not have (past its length, or an entry outside the pool, which is reported) is
 // loaded from beyond the pool's last page, where the tensor map reads zeros; so a tile always
 // brings all its bytes.  Rows of the last page past the user's length may hold anything.  For K that
 // is harmless, their scores are masked by selection; for V it is not (0 * NaN), so such a V tile
-// lands on its own barrier, this warp clears the rows, and only then does the group become ready.
+// lands on its own barrier, which all producers wait for, the first one clears the rows, and only then does
+// the group become ready.
 template <int D, class Ctl>
 __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                              const FwdParams& p, uint32_t sQ, uint32_t sKV, int lane) {
+                              const FwdParams& p, uint32_t sQ, uint32_t sKV, int lane, int who) {
   using Cfg = FwdCfg<D>;
   volatile int32_t* abort_flag = &ctl->abort_flag;
   auto bar = [](const uint64_t& b) { return ptx::smem_addr(&b); };
@@ -345,149 +354,174 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
   const PagedView& cache = p.paged.cache;
   const PagedPlan& plan = p.paged.plan;
   const int M = plan.header[1];
+  const bool chief = who == 0;
   const int page_rows = 1 << cache.page_shift;
   const int box_rows = page_rows < kTileRows ? page_rows : kTileRows;
-  const int boxes = kTileRows / box_rows;
-  const uint32_t box_off = (uint32_t)lane * box_rows * Cfg::kRowBytes;
+  const int boxes = kTileRows / box_rows;  // pages of a tile: 1, 2, 4, 8 or 16
+  // This lane's copy of a tile.
+  const int box = lane / Cfg::kBlocks, blk = lane % Cfg::kBlocks;
+  const bool holds = box < boxes, issues = holds && lane % kPagedProducers == who;
+  const uint32_t box_off = (uint32_t)(blk * Cfg::kBlockBytes + box * box_rows * Cfg::kRowBytes);
 
-  // Where lane l's box of a tile comes from (held: the user has that page), and for V how many rows of
-  // the tile to keep.
+  // Where a tile comes from (page: this lane's), and how many rows of a V tile are not to be cleared.
   struct Source {
     int page, row, h, keep;
-    bool held;
   };
   int slot = 0;
-  uint32_t sched_empty_par = (1u << kSlots) - 1u, tail_par = 0u;
+  uint32_t sched_par = chief ? (1u << kSlots) - 1u : 0u, tail_par = 0u;
   int sub = 0, j = 0, g = 0, armed_hi = 0;
+  uint32_t ring = 0;                 // ring slot of load j
+  int commit = 1;                    // score commit that frees the next group's two ring slots: group
+  uint32_t commit_par = 0u;          // g - kStages / 2's, and its phase (first waited for as group 1)
   bool loose = false;
   Source v0{}, v1{}, v2{};  // V tiles g-3, g-2, g-1
   bool ok = true;
-  auto slot_free = [&](int e) {
-    if (e < Cfg::kStages) return true;
-    const int G = group_of_load(e - Cfg::kStages);
-    return wait_all(bar(ctl->s_full[G % kSCommits]), (uint32_t)((G / kSCommits) & 1));
-  };
   auto copy = [&](const CUtensorMap* tm, uint32_t dst, uint32_t rb, const Source& s) {
-    if (lane < boxes) {
-      for (int blk = 0; blk < Cfg::kBlocks; ++blk)
-        ptx::tma_load_4d(dst + blk * Cfg::kBlockBytes + box_off, tm, rb, blk * Cfg::kBlockElems, s.row, s.h, s.page);
-    }
+    if (issues) ptx::tma_load_4d(dst + box_off, tm, rb, blk * Cfg::kBlockElems, s.row, s.h, s.page);
   };
-  auto ring = [&](int e) { return sKV + (e % Cfg::kStages) * Cfg::kTileBytes; };
-  // The next V tile, the next K tile or both, in this order, onto the group barrier rb, and the producer's
+  // The next V tile, the next K tile or both, in this order, onto the group barrier rb, and the chief's
   // arrival there.
-  auto arm = [&](uint32_t rb, bool has_v, const Source v, bool has_k, const Source k) {
+  auto arm = [&](uint32_t rb, bool has_v, const Source& v, bool has_k, const Source& k) {
     const uint32_t k_bytes = has_k ? Cfg::kTileBytes : 0u;
     const bool clear = has_v && v.keep < kTileRows;
-    if (lane == 0) {
-      if (clear) {
-        if (k_bytes) ptx::mbar_expect_tx(rb, k_bytes);
-        ptx::mbar_arrive_expect_tx(bar(ctl->v_tail), Cfg::kTileBytes);
-      } else {
-        ptx::mbar_arrive_expect_tx(rb, k_bytes + (has_v ? Cfg::kTileBytes : 0u));
-        if (!has_v)  // no P.V in this group: stand in for the SiLU warps' arrivals
-          for (int a = 0; a < 4; ++a) ptx::mbar_arrive(rb);
+    if (chief) {
+      if (lane == 0) {
+        if (clear) {
+          if (k_bytes) ptx::mbar_expect_tx(rb, k_bytes);
+          ptx::mbar_arrive_expect_tx(bar(ctl->v_tail), Cfg::kTileBytes);
+        } else {
+          ptx::mbar_arrive_expect_tx(rb, k_bytes + (has_v ? Cfg::kTileBytes : 0u));
+          if (!has_v)  // no P.V in this group: stand in for the SiLU warps' arrivals
+            for (int a = 0; a < 4; ++a) ptx::mbar_arrive(rb);
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
-    const uint32_t vdst = ring(j);
+    auto next_slot = [&] {
+      const uint32_t at = sKV + ring * Cfg::kTileBytes;
+      ++j;
+      ring = ring + 1 == Cfg::kStages ? 0 : ring + 1;
+      return at;
+    };
+    uint32_t vdst = 0;
     if (has_v) {
+      vdst = next_slot();
       copy(tm_v, vdst, clear ? bar(ctl->v_tail) : rb, v);
-      ++j;
     }
-    if (has_k) {
-      copy(tm_k, ring(j), rb, k);
-      ++j;
-    }
+    if (has_k) copy(tm_k, next_slot(), rb, k);
     if (clear) {
       loose = true;
       if (!wait_all(bar(ctl->v_tail), tail_par)) return false;
       tail_par ^= 1u;
-      const uint32_t off = (uint32_t)v.keep * Cfg::kRowBytes;
-      for (uint32_t x = off + lane * 16; x < (uint32_t)Cfg::kBlockBytes; x += 32 * 16)
-        for (int blk = 0; blk < Cfg::kBlocks; ++blk) ptx::st_shared_v4(vdst + blk * Cfg::kBlockBytes + x, 0, 0, 0, 0);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(rb);
+      if (chief) {
+        const uint32_t off = (uint32_t)v.keep * Cfg::kRowBytes;
+        for (uint32_t x = off + lane * 16; x < (uint32_t)Cfg::kBlockBytes; x += 32 * 16)
+          for (int c = 0; c < Cfg::kBlocks; ++c) ptx::st_shared_v4(vdst + c * Cfg::kBlockBytes + x, 0, 0, 0, 0);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(rb);
+      }
     }
     loose = false;
     return true;
   };
 
   while (ok) {
-    int idx = 0;
-    if (lane == 0) idx = atomicAdd(p.work_counter, 1);
-    idx = __shfl_sync(0xffffffffu, idx, 0);
-    const bool valid = idx < M;
-    PagedPiece pc{};
-    int q_row0 = 0, pos0 = 0, nrows = 0, L = 0, U = 0;
-    if (valid) {
-      const int4* at = reinterpret_cast<const int4*>(plan.pieces + idx);
-      const int4 a = at[0], b = at[1];
-      pc = PagedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      if (pc.tiles == 0) continue;
-      const int q0 = p.q_start[pc.b], n = p.q_start[pc.b + 1] - q0;
-      L = p.paged.kv_len[pc.b];
-      U = L - (p.num_targets ? p.num_targets[pc.b] : 0);
-      q_row0 = q0 + pc.block * kItemRows;
-      pos0 = L - n + pc.block * kItemRows;
-      nrows = min(n - pc.block * kItemRows, kItemRows);
+    Work w{};
+    Piece pc{};
+    int b = 0;
+    if (chief) {
+      int idx = 0;
+      if (lane == 0) idx = atomicAdd(p.work_counter, 1);
+      idx = __shfl_sync(0xffffffffu, idx, 0);
+      w.valid = idx < M;
+      if (w.valid) {
+        const int4* at = reinterpret_cast<const int4*>(plan.pieces + idx);
+        const int4 x = at[0], y = at[1];
+        const PagedPiece pp{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        if (pp.tiles == 0) continue;
+        b = pp.b;
+        pc = Piece{pp.tile0, pp.tiles, pp.parts, pp.part, pp.pitch};
+        const int q0 = p.q_start[b], n = p.q_start[b + 1] - q0;
+        w.h = pp.h;
+        w.kv_start = idx - pp.part * pp.pitch;
+        w.L = p.paged.kv_len[b];
+        w.U = w.L - (p.num_targets ? p.num_targets[b] : 0);
+        w.q_row0 = q0 + pp.block * kItemRows;
+        w.pos0 = w.L - n + pp.block * kItemRows;
+        w.nrows = min(n - pp.block * kItemRows, kItemRows);
+      }
+      if (!wait_all(bar(ctl->sched_empty[slot]), (sched_par >> slot) & 1u)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        volatile int32_t* s = ctl->slot[slot];
+        s[0] = w.valid; s[1] = w.h; s[2] = w.kv_start; s[3] = w.q_row0;
+        s[4] = w.pos0; s[5] = w.nrows; s[6] = w.L; s[7] = w.U;
+        s[8] = pc.tile0; s[9] = pc.tiles; s[10] = pc.parts; s[11] = pc.part;
+        s[12] = pc.pitch; s[13] = b;
+        ptx::mbar_arrive(bar(ctl->sched_full[slot]));
+      }
+    } else {
+      if (!wait_all(bar(ctl->sched_full[slot]), (sched_par >> slot) & 1u)) {
+        ok = false;
+        break;
+      }
+      w = read_slot(ctl->slot[slot]);
+      pc = read_piece(ctl->slot[slot]);
+      b = *(volatile int32_t*)&ctl->slot[slot][13];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(ctl->sched_empty[slot]));
     }
-    if (!wait_all(bar(ctl->sched_empty[slot]), (sched_empty_par >> slot) & 1u)) {
-      ok = false;
-      break;
-    }
-    sched_empty_par ^= 1u << slot;
-    if (lane == 0) {
-      volatile int32_t* s = ctl->slot[slot];
-      s[0] = valid; s[1] = pc.h; s[2] = idx - pc.part * pc.pitch; s[3] = q_row0;
-      s[4] = pos0; s[5] = nrows; s[6] = L; s[7] = U;
-      s[8] = pc.tile0; s[9] = pc.tiles; s[10] = pc.parts; s[11] = pc.part;
-      s[12] = pc.pitch;
-      ptx::mbar_arrive(bar(ctl->sched_full[slot]));
-    }
+    sched_par ^= 1u << slot;
     slot = (slot + 1) & (kSlots - 1);
-    if (!valid) break;
+    if (!w.valid) break;
 
-    const int32_t* table = cache.table + pc.b * cache.table_ld;
-    const TileRange r = key_tiles(pos0, pos0 + nrows, U);
+    const int32_t* table = cache.table + b * cache.table_ld;
+    const TileRange r = key_tiles(w.pos0, w.pos0 + w.nrows, w.U);
     // Only loads the table entry: it is looked at when the tile's turn comes.
-    auto source = [&](int k) {
-      const int key0 = tile_at(r, pc.tile0 + k) * kTileRows, key = key0 + lane * box_rows;
-      Source s;
-      s.h = pc.h;
-      s.row = key & (page_rows - 1);
-      s.held = lane < boxes && key < L;
-      s.page = cache.num_pages;
-      if (s.held) s.page = table[key >> cache.page_shift];
-      // Whole pages past the length come as zeros already.
-      s.keep = L - key0 < kTileRows && (L & (box_rows - 1)) != 0 ? L - key0 : kTileRows;
-      return s;
+    auto look_up = [&](int k) {
+      const int key = tile_at(r, pc.tile0 + k) * kTileRows + box * box_rows;
+      return holds && key < w.L ? table[key >> cache.page_shift] : -1;
     };
-    Source ahead = source(0);
-    const int qb = sub % Cfg::kQBufs;
-    if (!wait_all(bar(ctl->q_empty[qb]), (uint32_t)(((sub / Cfg::kQBufs) & 1) ^ 1))) {
-      ok = false;
-      break;
+    int ahead = look_up(0);
+    if (chief) {
+      const int qb = sub % Cfg::kQBufs;
+      if (!wait_all(bar(ctl->q_empty[qb]), (uint32_t)(((sub / Cfg::kQBufs) & 1) ^ 1))) {
+        ok = false;
+        break;
+      }
+      loose = true;  // until group g is armed
+      if (lane == 0) {
+        const uint32_t rb = bar(ctl->g_ready[g & (kGroupBars - 1)]);
+        ptx::mbar_expect_tx(rb, Cfg::kTileBytes);
+        for (int c = 0; c < Cfg::kBlocks; ++c)
+          ptx::tma_load_2d(sQ + qb * Cfg::kTileBytes + c * Cfg::kBlockBytes, tm_q, rb, w.h * D + c * Cfg::kBlockElems,
+                           w.q_row0);
+      }
+      ++sub;
     }
-    loose = true;  // until group g is armed
-    if (lane == 0) {
-      const uint32_t rb = bar(ctl->g_ready[g & (kGroupBars - 1)]);
-      ptx::mbar_expect_tx(rb, Cfg::kTileBytes);
-      for (int blk = 0; blk < Cfg::kBlocks; ++blk)
-        ptx::tma_load_2d(sQ + qb * Cfg::kTileBytes + blk * Cfg::kBlockBytes, tm_q, rb, pc.h * D + blk * Cfg::kBlockElems,
-                         q_row0);
-    }
-    ++sub;
     for (int k = 0; k < pc.tiles; ++k) {
       const bool has_v = g >= 3;
-      if (!slot_free(j) || (has_v && !slot_free(j + 1))) { ok = false; break; }
-      Source here = ahead;
-      if (k + 1 < pc.tiles) ahead = source(k + 1);
-      if (here.held && (unsigned)here.page >= (unsigned)cache.num_pages) {
-        atomicOr(p.err, kErrBadOffsets);
+      // Group g's loads are 2 g - 3 and 2 g - 2; the ring slots' last tiles were consumed by group
+      // g - kStages / 2 at the latest (group_of_load), whose score commit covers both.
+      if (j + (has_v ? 1 : 0) >= Cfg::kStages) {
+        if (!wait_all(bar(ctl->s_full[commit]), commit_par)) { ok = false; break; }
+        if (++commit == kSCommits) {
+          commit = 0;
+          commit_par ^= 1u;
+        }
+      }
+      const int key0 = tile_at(r, pc.tile0 + k) * kTileRows;
+      Source here{ahead, boxes > 1 ? 0 : key0 & (page_rows - 1), w.h, kTileRows};
+      if (k + 1 < pc.tiles) ahead = look_up(k + 1);
+      if ((unsigned)here.page >= (unsigned)cache.num_pages) {
+        if (issues && key0 + box * box_rows < w.L) atomicOr(p.err, kErrBadOffsets);
         here.page = cache.num_pages;
       }
+      // Whole pages past the length come as zeros already.
+      if (w.L - key0 < kTileRows && (w.L & (box_rows - 1)) != 0) here.keep = w.L - key0;
       if (!arm(bar(ctl->g_ready[g & (kGroupBars - 1)]), has_v, v0, true, here)) { ok = false; break; }
       v0 = v1;
       v1 = v2;
@@ -499,18 +533,23 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
   for (int t = (g >= 3 ? g - 3 : 0); t < g && ok; ++t) {
     const int i = t - g + 3;  // 0, 1, 2 <-> tiles g-3, g-2, g-1
     const Source v = i == 0 ? v0 : (i == 1 ? v1 : v2);
-    if (!slot_free(j)) { ok = false; break; }
+    if (j >= Cfg::kStages) {
+      const int G = group_of_load(j - Cfg::kStages);
+      if (!wait_all(bar(ctl->s_full[G % kSCommits]), (uint32_t)((G / kSCommits) & 1))) { ok = false; break; }
+    }
     if (!arm(bar(ctl->g_ready[(t + 3) & (kGroupBars - 1)]), true, v, false, v)) { ok = false; break; }
     armed_hi = t + 4;
   }
-  if (lane == 0 && *abort_flag) drain_copies(ctl, g, armed_hi, loose);
+  // The other producers may have issued copies for a group that the first one never armed: they let the
+  // whole budget pass.
+  if (lane == 0 && *abort_flag) drain_copies(ctl, chief ? g : 0, chief ? armed_hi : 0, !chief || loose);
 }
 
 // kPaged: K and V come from a paged cache (tm_k, tm_v: 4-D maps of the pool) and the work from a
 // PagedPlan, whose pieces may be part of an item; produce_paged replaces the producer, and the
 // epilogue of a part writes fp32 sums.
 template <int D, bool kRab, bool kPaged = false>
-__global__ void __launch_bounds__(kNumThreads, 1)
+__global__ void __launch_bounds__(kPaged ? kPagedThreads : kNumThreads, 1)
     hstu_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
   using Cfg = FwdCfg<D>;
@@ -538,7 +577,8 @@ __global__ void __launch_bounds__(kNumThreads, 1)
     ptx::mbar_init(bar(ctl->o_empty), 4);      // one arrival per epilogue warp
     for (int s = 0; s < kSlots; ++s) {
       ptx::mbar_init(bar(ctl->sched_full[s]), 1);
-      ptx::mbar_init(bar(ctl->sched_empty[s]), 1 + 8 + 4);  // MMA, SiLU and epilogue warps
+      // MMA, SiLU, epilogue and further producer warps
+      ptx::mbar_init(bar(ctl->sched_empty[s]), 1 + 8 + 4 + (kPaged ? kPagedProducers - 1 : 0));
     }
     ptx::mbar_init(bar(ctl->drain), 1);
     if constexpr (kPaged) ptx::mbar_init(bar(ctl->v_tail), 1);
@@ -560,7 +600,7 @@ __global__ void __launch_bounds__(kNumThreads, 1)
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
     if constexpr (kPaged) {
-      produce_paged<D>(ctl, &tm_q, &tm_k, &tm_v, p, sQ, sKV, lane);
+      produce_paged<D>(ctl, &tm_q, &tm_k, &tm_v, p, sQ, sKV, lane, 0);
     } else if (lane == 0) {
       // Everything before this point touched only shared memory, TMEM and kernel parameters; the
       // plan (and q/k/v) come from the preceding grid.
@@ -680,6 +720,8 @@ __global__ void __launch_bounds__(kNumThreads, 1)
       }
     }
     __syncwarp();
+  } else if (kPaged && warp >= kPagedWarp0) {
+    produce_paged<D>(ctl, &tm_q, &tm_k, &tm_v, p, sQ, sKV, lane, warp - kPagedWarp0 + 1);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer
     // The whole warp runs this loop in step, so the control flow is uniform and the descriptors

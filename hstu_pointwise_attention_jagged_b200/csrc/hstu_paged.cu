@@ -320,7 +320,7 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   p.paged.partials = reinterpret_cast<float4*>(at + o_partials);
   e = launch_dependent(paged_schedule_kernel, 1, kSchedThreads, 0, 0, stream, s);
   if (e == cudaSuccess)
-    e = launch_dependent(hstu_fwd_kernel<D, false, true>, ctas, kNumThreads, FwdCfg<D>::kSmemBytes, 0, stream, tq, tk, tv, p);
+    e = launch_dependent(hstu_fwd_kernel<D, false, true>, ctas, kPagedThreads, FwdCfg<D>::kSmemBytes, 0, stream, tq, tk, tv, p);
   if (cudaFreeAsync(buf, stream) != cudaSuccess && e == cudaSuccess) return HSTU_ERR_CUDA;
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
