@@ -179,7 +179,38 @@ cudaError_t once_per_device(std::once_flag (&once)[kMaxDevices], cudaError_t (&r
   return result[dev];
 }
 
-// At most 16 rows a user.
+// How the few-rows kernels would take a call.
+struct RowsShape {
+  bool clustered;  // clusters of `cluster` CTAs (else equal runs)
+  int cluster;
+  bool few;        // the few-rows kernels are the ones to take it
+};
+
+// Clusters as large as keeps every CTA resident at once and busy with two tiles, if that leaves each CTA a
+// short stretch of tiles: then one launch does it all.  A long stretch takes the equal runs, which ragged
+// lengths cannot unbalance.  (us, d = 128, one row a user: 64 users x 4 heads of 700 rows, 11 tiles a CTA,
+// 18.2 against 24.0; 16 x 4 of 3000, 12 tiles, 20.3 against 24.2; 64 x 4 of ragged histories up to 4096,
+// 64 tiles, 62 against 41; 1 x 4 of 32000, 31 tiles, 29 against 20.)
+//
+// Users of 17 to 64 rows go here while the call is short; otherwise every block of 16 rows reading all
+// keys costs more than the tcgen05 kernel's plan and fill.
+RowsShape rows_shape(const RowsArgs& a, int keys, int num_sms) {
+  const int64_t items = static_cast<int64_t>(a.B) * a.H * a.blocks;
+  const int64_t tiles = a.max_kv / keys + 1;  // of an item, at most
+  RowsShape s;
+  s.cluster = 1;
+  while (s.cluster < kRowsMaxSplit && 2 * s.cluster * items <= 2 * num_sms && 4 * s.cluster <= tiles) s.cluster *= 2;
+  const int64_t stretch = (tiles + s.cluster - 1) / s.cluster;
+  s.clustered = stretch <= kRowsClusterTiles || a.B > kRunUsers || items * tiles > INT_MAX;
+  s.few = a.blocks == 1;
+  if (a.blocks > 1) {
+    s.few = a.max_new <= kRowsMaxNew && stretch <= kRowsBlocksTiles && items * tiles <= 2 * num_sms * kRowsBlocksTiles;
+    s.clustered = true;
+  }
+  return s;
+}
+
+// A few rows a user.
 template <int D>
 hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t stream) {
   using Cfg = RowsCfg<D>;
@@ -193,18 +224,12 @@ hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t
     return r;
   });
   if (e != cudaSuccess) return HSTU_ERR_CUDA;
-  const int64_t items = static_cast<int64_t>(a.B) * a.H;
-  const int64_t tiles = a.max_kv / Cfg::kKeys + 1;  // of an item, at most
-  // Clusters as large as keeps every CTA resident at once and busy with two tiles, if that leaves each CTA a
-  // short stretch of tiles: then one launch does it all.  A long stretch takes the equal runs, which ragged
-  // lengths cannot unbalance.  (us, d = 128, one row a user: 64 users x 4 heads of 700 rows, 11 tiles a CTA,
-  // 18.2 against 24.0; 16 x 4 of 3000, 12 tiles, 20.3 against 24.2; 64 x 4 of ragged histories up to 4096,
-  // 64 tiles, 62 against 41; 1 x 4 of 32000, 31 tiles, 29 against 20.)
-  int cluster = 1;
-  while (cluster < kRowsMaxSplit && 2 * cluster * items <= 2 * st.num_sms && 4 * cluster <= tiles) cluster *= 2;
-  if ((tiles + cluster - 1) / cluster <= kRowsClusterTiles || a.B > kRunUsers || items * tiles > INT_MAX) {
-    if (items * cluster > INT_MAX) return HSTU_ERR_UNSUPPORTED;
-    e = launch_dependent(paged_rows_kernel<D>, items * cluster, kRowsThreads, Cfg::kSmemBytes, cluster, stream, a);
+  const RowsShape shape = rows_shape(a, Cfg::kKeys, st.num_sms);
+  const int64_t items = static_cast<int64_t>(a.B) * a.H * a.blocks;
+  if (shape.clustered) {
+    if (items * shape.cluster > INT_MAX) return HSTU_ERR_UNSUPPORTED;
+    e = launch_dependent(paged_rows_kernel<D>, items * shape.cluster, kRowsThreads, Cfg::kSmemBytes, shape.cluster, stream,
+                         a);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   const int runs = 2 * st.num_sms;
@@ -443,13 +468,15 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
   a.B = B;
   a.H = H;
   a.total_new = total_new;
-  a.max_new = max_new;
   a.max_kv = max_kv;
   a.half_alpha = 0.5f * alpha;
   a.inv_n = 1.0f / N;
   a.err = st->err_word;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if ((max_new < total_new ? max_new : total_new) > kRowsBlock)
+  const int32_t most = max_new < total_new ? max_new : total_new;
+  a.blocks = most > kRowsBlock ? (most + kRowsBlock - 1) / kRowsBlock : 1;
+  a.max_new = most;
+  if (!rows_shape(a, 64 * 128 / d, st->num_sms).few)
     return d == 128 ? launch_many<128>(a, *cache, alpha, *st, cs)
                     : (d == 64 ? launch_many<64>(a, *cache, alpha, *st, cs) : launch_many<32>(a, *cache, alpha, *st, cs));
   return d == 128 ? launch_rows<128>(a, *st, cs) : (d == 64 ? launch_rows<64>(a, *st, cs) : launch_rows<32>(a, *st, cs));

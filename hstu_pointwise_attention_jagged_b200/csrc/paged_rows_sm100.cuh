@@ -17,6 +17,7 @@
 //   paged_rows_kernel      one cluster of CTAs for each item; the partial O's are added over distributed
 //                          shared memory, in rank order.  One launch and no workspace: for calls whose
 //                          time is latency, and for batches of so many items that each needs one CTA.
+//                          Up to 64 rows a user become several items if the call stays short.
 //   paged_rows_run_kernel  the tiles of all items, in item order, dealt out in equal runs to two CTAs for
 //                          each SM; parts of items go to a workspace and paged_rows_sum_kernel adds them in
 //                          order.  Ragged lengths and any number of items load every SM alike.
@@ -34,10 +35,12 @@
 namespace hstu {
 
 constexpr int kRowsThreads = 128;
-constexpr int kRowsBlock = 16;        // query rows of a user at most
+constexpr int kRowsBlock = 16;        // query rows of a CTA
+constexpr int kRowsMaxNew = 64;       // rows of a user at most
 constexpr int kRowsStages = 3;
 constexpr int kRowsMaxSplit = 16;     // CTAs of a cluster
-constexpr int kRowsClusterTiles = 16; // tiles of a CTA of a cluster at most
+constexpr int kRowsClusterTiles = 16; // tiles of a CTA of a cluster at most, for one block of rows a user
+constexpr int kRowsBlocksTiles = 8;   // ... and for several
 
 template <int D>
 struct RowsCfg {
@@ -66,6 +69,7 @@ struct RowsArgs {
   const int32_t* kv_len;
   const int32_t* num_targets;  // may be null
   int32_t B, H, total_new, max_new, max_kv;
+  int32_t blocks;  // 16-row blocks of a user's rows, at most; an item is one of them
   float half_alpha, inv_n;
   unsigned* err;
 };
@@ -261,19 +265,22 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsA
   const int split = (int)ptx::cluster_ctarank();
   const int S = (int)(gridDim.x / ptx::nclusters_x());
   const int item = (int)ptx::cluster_id_x();
-  const int b = item / p.H, h = item - b * p.H;
+  const int bh = item / p.blocks, blk = item - bh * p.blocks;
+  const int b = bh / p.H, h = bh - b * p.H;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedUser u = paged_user(p.cache, p.q_offsets, p.kv_len, p.num_targets, b, p.total_new, p.max_new, p.max_kv);
-  if (split == 0 && h == 0 && tid == 0) {
+  if (split == 0 && h == 0 && blk == 0 && tid == 0) {
     bool bad = !u.ok;
     if (b == 0) bad |= p.q_offsets[0] != 0 || p.q_offsets[p.B] != p.total_new;
     if (bad) atomicOr(p.err, kErrBadOffsets);
   }
-  if (!u.ok || u.n == 0) return;  // the whole cluster agrees
+  const int r0 = blk * kRowsBlock, nrows = min(kRowsBlock, u.n - r0);
+  if (!u.ok || nrows <= 0) return;  // the whole cluster agrees
+  const int row0 = u.q0 + r0, pos0 = u.L - u.n + r0;
 
   // This CTA's share of the visible key tiles.
-  const TileRange range = key_tiles<Cfg::kKeys>(u.L - u.n, u.L, u.L - u.T);
+  const TileRange range = key_tiles<Cfg::kKeys>(pos0, pos0 + nrows, u.L - u.T);
   const int ntiles = tile_count(range);
   const int t_begin = (int)((int64_t)ntiles * split / S), t_end = (int)((int64_t)ntiles * (split + 1) / S);
 
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsA
 #pragma unroll
   for (int s = 0; s < kRowsStages - 1; ++s) fetch(t_begin + s, s);
   RowsQuery<D> q;
-  q.load(p.q + (int64_t)u.q0 * p.q_ld + (int64_t)h * D, p.q_ld, u.n, u.L - u.n, u.L - u.T);
+  q.load(p.q + (int64_t)row0 * p.q_ld + (int64_t)h * D, p.q_ld, nrows, pos0, u.L - u.T);
   float o[D / 8][4];
   rows_clear<D>(o);
 
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsA
     *reinterpret_cast<float2*>(at + 8 * kPitch) = make_float2(o[j][2], o[j][3]);
   }
   __syncthreads();
-  const int quads = u.n * (D / 4);
+  const int quads = nrows * (D / 4);
   for (int i = tid; i < quads; i += kRowsThreads) {
     const int r = i / (D / 4), c = i % (D / 4);
     float4* at = reinterpret_cast<float4*>(part) + r * kQuads + c;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsA
 #pragma unroll
     for (int w = 1; w < 4; ++w) a = add4(a, at[w * kRowsBlock * kQuads]);
     if (S > 1) *at = a;
-    else rows_store<D>(p, u.q0 + r, h, c, a);
+    else rows_store<D>(p, row0 + r, h, c, a);
   }
   if (S == 1) return;
   ptx::cluster_sync();
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsA
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
     for (int w = 0; w < S; ++w) a = add4(a, ptx::ld_cluster_v4(ptx::mapa_shared(sbase + (r * kQuads + c) * 16, w)));
-    rows_store<D>(p, u.q0 + r, h, c, a);
+    rows_store<D>(p, row0 + r, h, c, a);
   }
   ptx::cluster_sync();  // no CTA leaves while its sums are read
 }

@@ -28,7 +28,7 @@ struct PagedSchedArgs {
   const int32_t* q_offsets;
   const int32_t* kv_len;
   const int32_t* num_targets;
-  int32_t B, H, total_new, max_new, max_kv, nbins, nwaves, wave_rows, num_ctas, max_items, max_cut;
+  int32_t B, H, total_new, max_new, max_kv, nbins, nwaves, wave_rows, num_ctas, max_items, max_cut;  // max_items: H * (total_new / 128 + B)
   PagedPlan plan;
   unsigned* err;
 };
@@ -40,15 +40,17 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   __shared__ int hist[kMaxCostBins];
   __shared__ long long scan_scratch[2][32];
   __shared__ long long carry_blocks, carry_rows;
+  __shared__ int first_bad;  // first user whose offsets decrease
   __shared__ int longest, pieces_of[kMaxCuts + 1];
   __shared__ PagedUser s_user[kCachedUsers];
-  __shared__ int s_start[kCachedUsers + 1], s_wave[kCachedUsers];
+  __shared__ int s_start[kCachedUsers + 1], s_wave[kCachedUsers], s_cost[kCachedUsers];
   const bool cached = a.B <= kCachedUsers;
   const int tid = threadIdx.x;
   if (tid == 0) {
     carry_blocks = 0;
     carry_rows = 0;
     longest = 0;
+    first_bad = INT_MAX;
   }
   if (tid <= kMaxCuts) pieces_of[tid] = 0;
   __syncthreads();
@@ -64,7 +66,12 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
       if (b == 0) bad |= u.q0 != 0;
       if (b == a.B - 1) bad |= a.q_offsets[a.B] != a.total_new;
       if (bad) atomicOr(a.err, kErrBadOffsets);
-      if (!u.ok) u.n = u.L = 0;
+      if (a.q_offsets[b + 1] < u.q0) atomicMin(&first_bad, b);
+    }
+    __syncthreads();
+    if (b < a.B) {
+      // Behind decreasing offsets users may overlap, and their blocks be more than the plan has room for.
+      if (!u.ok || b >= first_bad) u.n = u.L = 0;
       blocks = cdiv(u.n, kItemRows);
       rows = u.n > 0 ? u.L : 0;
     }
@@ -78,6 +85,7 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
         s_user[b] = u;
         s_start[b] = start;
         s_wave[b] = (int)(wave < a.nwaves ? wave : a.nwaves - 1);
+        s_cost[b] = 0;
       }
     }
     __syncthreads();
@@ -93,10 +101,7 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     if (cached) s_start[a.B] = nblocks;
   }
   __syncthreads();
-  // Overlapping (inconsistent) offsets can make the users' blocks more than the plan has room for; the
-  // surplus is dropped, and was reported.
-  const int64_t items64 = (int64_t)nblocks * a.H;
-  const int items = (int)(items64 < a.max_items ? items64 : a.max_items);
+  const int items = nblocks * a.H;  // at most a.max_items
   // Block g: its user, index within the user and tiles.
   auto block_of = [&](int g, int& b, int& blk) {
     b = owner_of(cached ? s_start : a.plan.block_start, a.B, g);
@@ -108,31 +113,27 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     return item_cost(u.L - u.n + blk * kItemRows, rows < kItemRows ? rows : kItemRows, u.L - u.T);
   };
 
-  if (cached && items <= a.max_cut) {
-    // Most tiles of an item, for each user (s_wave) and in all.
-    if (tid < a.B) s_wave[tid] = 0;
-    __syncthreads();
+  // Cuts that can be tried: c pieces of every item may not be more than there is room for.
+  const int most = items > 0 ? min(kMaxCuts, a.max_cut / items) : 1;
+  if (cached && most > 1) {
+    // Most tiles of an item, for each user (s_cost) and in all.
     for (int g = tid; g < nblocks; g += kSchedThreads) {
       int b, blk;
       const int cost = block_of(g, b, blk);
-      atomicMax(&s_wave[b], cost);
+      atomicMax(&s_cost[b], cost);
       atomicMax(&longest, cost);
     }
     __syncthreads();
-    // Pieces when the longest item is cut in c, for c = 1 .. kMaxCuts.
+    // Pieces when the longest item is cut in c.
     const int top = longest;
-    if (tid < a.B) {
-      const int64_t rows = (int64_t)(s_start[tid + 1] - s_start[tid]) * a.H;
-#pragma unroll
-      for (int c = 1; c <= kMaxCuts; ++c) {
-        const int64_t n = rows * cdiv(s_wave[tid], cdiv(top, c));
-        if (n) atomicAdd(&pieces_of[c], (int)(n < a.max_cut + 1 ? n : a.max_cut + 1));
-      }
+    if (tid < a.B && s_cost[tid] > 0) {
+      const int rows = (s_start[tid + 1] - s_start[tid]) * a.H;
+      for (int c = 1; c <= most; ++c) atomicAdd(&pieces_of[c], rows * cdiv(s_cost[tid], cdiv(top, c)));
     }
     __syncthreads();
     // The best c by estimated time, ties to the smaller: lane c - 1 of each warp rates c.
     int best = (tid & 31) + 1, time = INT_MAX;
-    if (best <= kMaxCuts && best <= top && pieces_of[best] <= a.max_cut) {
+    if (best <= most && best <= top && pieces_of[best] <= a.max_cut) {
       const int q = cdiv(top, best);
       if (best == 1 || q >= kMinPieceTiles)
         time = cdiv(pieces_of[best], a.num_ctas) * (q + (best > 1 ? kPieceOverhead : 0));
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
       // that a short item does not have stay empty.
       const int q = cdiv(top, best);
       long long mine = 0, tot;
-      if (tid < a.B) mine = (long long)(s_start[tid + 1] - s_start[tid]) * a.H * cdiv(s_wave[tid], q);
+      if (tid < a.B) mine = (long long)(s_start[tid + 1] - s_start[tid]) * a.H * cdiv(s_cost[tid], q);
       const int first = (int)(block_inclusive_scan(mine, scan_scratch[0], &tot) - mine);
       if (tid < a.B) hist[tid] = first;
       __syncthreads();
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
         PagedPiece p;
         p.h = x / nblocks;
         const int cost = block_of(x - p.h * nblocks, p.b, p.block);
-        const int parts = cdiv(s_wave[p.b], q);
+        const int parts = cdiv(s_cost[p.b], q);
         p.pitch = s_start[p.b + 1] - s_start[p.b];
         p.parts = min(parts, cost);
         const int at = hist[p.b] + p.h * parts * p.pitch + p.block;
@@ -176,13 +177,11 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
       }
       return;
     }
-    // Whole items after all: one wave.
-    if (tid < a.B) s_wave[tid] = 0;
-    __syncthreads();
   }
 
   // Whole items, as schedule_kernel: a counting sort of the blocks by (wave, non-increasing cost).
-  const int nkeys = a.nbins * a.nwaves;
+  const long long waves = (carry_rows + a.wave_rows - 1) / a.wave_rows;  // that the batch reaches
+  const int nkeys = a.nbins * (int)(cached && waves < a.nwaves ? (waves > 0 ? waves : 1) : a.nwaves);
   for (int i = tid; i < nkeys; i += kSchedThreads) hist[i] = 0;
   __syncthreads();
   auto key_of = [&](int b, int cost) {

@@ -66,6 +66,8 @@ SMALL = [
 ]
 LARGE = [
     ([(0, 17, 0)], 16, 1, "rows"),
+    ([(0, 17, 0), (127, 1, 1), (0, 1, 0), (128, 16, 2), (5, 0, 0), (3, 64, 64)], 8, 2, "rows"),
+    ([(300, 64, 3), (2000, 33, 33), (1, 63, 0)], 32, 1, "halves"),
     ([(0, 300, 40), (129, 128, 0), (128, 129, 1), (1000, 0, 0), (7, 257, 257), (513, 1, 0)], 16, 2, "rows"),
     ([(0, 128, 128), (384, 127, 3), (640, 200, 100)], 64, 3, "heads"),
     ([(900, 600, 500), (0, 64, 0)], 256, 1, "halves"),
@@ -91,6 +93,7 @@ def test_many_rows(case, d):
     users, page, H, layout = LARGE[case]
     x = Batch(users, page, H, d, layout, seed=case + 11)
     x.check(x.run())
+    x.check(x.run(max_new=5000, max_kv=9000))  # bounds that rule out the few-rows form
     assert binding.hstu_attn_get_error() == 0
 
 
