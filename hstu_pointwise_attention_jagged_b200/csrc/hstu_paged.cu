@@ -63,7 +63,7 @@ hstu_status_t check_rotation(const hstu_rotation_t* r, int32_t d, int64_t rows, 
   return HSTU_OK;
 }
 
-hstu_status_t check_cache(const hstu_paged_cache_t* c, int32_t H, int32_t d) {
+hstu_status_t check_cache(const hstu_paged_cache_t* c, int32_t d) {
   if (!c || !c->k || !c->v || c->num_pages < 1 || c->table_width < 0 || c->table_ld < c->table_width)
     return HSTU_ERR_INVALID_ARGUMENT;
   if (c->table_width > 0 && !c->page_table) return HSTU_ERR_INVALID_ARGUMENT;
@@ -75,7 +75,6 @@ hstu_status_t check_cache(const hstu_paged_cache_t* c, int32_t H, int32_t d) {
   }
   if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u))
     return HSTU_ERR_UNSUPPORTED;
-  (void)H;
   return HSTU_OK;
 }
 
@@ -394,9 +393,10 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
   using namespace hstu;
   if (B < 0 || H < 1 || total_new < 0) return HSTU_ERR_INVALID_ARGUMENT;
   if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4) return HSTU_ERR_UNSUPPORTED;
-  hstu_status_t s = check_cache(cache, H, d);
+  hstu_status_t s = check_cache(cache, d);
   if (s == HSTU_OK && rotation) s = check_rotation(rotation, d, total_new, false);
-  if (s != HSTU_OK || total_new == 0 || B == 0) return s;
+  if (s != HSTU_OK || total_new == 0) return s;
+  if (B == 0) return HSTU_ERR_INVALID_ARGUMENT;  // rows of no user
   if (!k || !v || !q_offsets || !kv_len) return HSTU_ERR_INVALID_ARGUMENT;
   if ((q == nullptr) != (q_out == nullptr) || (q && !rotation)) return HSTU_ERR_INVALID_ARGUMENT;
   const int64_t width = static_cast<int64_t>(H) * d;
@@ -444,8 +444,9 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
   if (!std::isfinite(alpha) || !std::isfinite(N) || !(N > 0.0f)) return HSTU_ERR_INVALID_ARGUMENT;
   if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4 || max_kv > INT_MAX - 4096)
     return HSTU_ERR_UNSUPPORTED;
-  hstu_status_t s = check_cache(cache, H, d);
-  if (s != HSTU_OK || total_new == 0 || B == 0) return s;
+  hstu_status_t s = check_cache(cache, d);
+  if (s != HSTU_OK || total_new == 0) return s;
+  if (B == 0) return HSTU_ERR_INVALID_ARGUMENT;  // rows of no user
   if (!q || !q_offsets || !kv_len || !out) return HSTU_ERR_INVALID_ARGUMENT;
   const int64_t width = static_cast<int64_t>(H) * d;
   if ((s = check_ld(q_ld, width)) != HSTU_OK || (s = check_ld(out_ld, width)) != HSTU_OK) return s;

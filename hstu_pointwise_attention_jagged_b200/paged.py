@@ -63,12 +63,16 @@ def _call(name, index, stream, *args):
 
 
 def _first(name, t):
-    """(rows, H, d, device index) of the call's first token tensor."""
+    """Shape, row stride (elements) and device index of the call's first token tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype is not _BF16 or t.dim() != 3:
+    shape = t.shape
+    if t.dtype is not _BF16 or len(shape) != 3:
         raise TypeError("%s must be a bf16 tensor [rows, H, d]" % name)
-    return (*t.shape, t.get_device())
+    index, s = t.get_device(), t.stride()
+    if s[2] == 1 and s[1] == shape[2] and shape[0] > 1:
+        return shape, s[0], index
+    return shape, _row_stride_slow(name, t, shape, index), index
 
 
 def _row_stride(name, t, shape, index):
@@ -93,6 +97,19 @@ def _row_stride_slow(name, t, shape, index):
     if n and ((c > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != c)):
         raise TypeError("%s must have its heads packed (only the row stride is free)" % name)
     return t.stride(0) if n > 1 else h * c  # the stride of a single row is never used
+
+
+def _output(name, t, shape, index, like, stream):
+    """The given output, or a new packed one, and its row stride.  A new one belongs to the stream that the
+    call runs on: memory of another stream might still be in use there."""
+    if t is not None:
+        return t, _row_stride(name, t, shape, index)
+    if stream is None:
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    return t, shape[1] * shape[2]
 
 
 def _index(name, t, n, index):
@@ -176,17 +193,14 @@ def hstu_rotary(q, k, positions, freqs, sections=None, interleaved=False, invers
     ``positions``: int32 [rows] or [axes, rows]; ``sections``: pairs of each axis.  ``inverse`` turns
     back, which is the gradient.  ``q_out`` may be q (in place).  See include/hstu_paged.h."""
     load_library()
-    rows, H, d, index = _first("q", q)
-    shape = (rows, H, d)
-    q_ld = _row_stride("q", q, shape, index)
+    shape, q_ld, index = _first("q", q)
+    rows, H, d = shape
     rot = _rotation(freqs, sections, positions, interleaved, rows, index, True)
-    q_out = q.new_empty(shape) if q_out is None else q_out
-    qo_ld = _row_stride("q_out", q_out, shape, index)
+    q_out, qo_ld = _output("q_out", q_out, shape, index, q, stream)
     k_ld = ko_ld = k_at = ko_at = 0
     if k is not None:
         k_ld = _row_stride("k", k, shape, index)
-        k_out = q.new_empty(shape) if k_out is None else k_out
-        ko_ld = _row_stride("k_out", k_out, shape, index)
+        k_out, ko_ld = _output("k_out", k_out, shape, index, q, stream)
         k_at, ko_at = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -202,9 +216,8 @@ def hstu_paged_append(k, v, k_cache, v_cache, page_table, q_offsets, kv_len, q=N
     given; ``positions`` default to the place in the cache.  Returns the rotated q (or None).
     See include/hstu_paged.h."""
     load_library()
-    total, H, d, index = _first("k", k)
-    shape = (total, H, d)
-    k_ld = _row_stride("k", k, shape, index)
+    shape, k_ld, index = _first("k", k)
+    total, H, d = shape
     v_ld = _row_stride("v", v, shape, index)
     B = _users(q_offsets)
     off, lens = _index("q_offsets", q_offsets, B + 1, index), _index("kv_len", kv_len, B, index)
@@ -216,8 +229,7 @@ def hstu_paged_append(k, v, k_cache, v_cache, page_table, q_offsets, kv_len, q=N
         raise ValueError("q, positions and sections need freqs")
     if q is not None:
         q_ld = _row_stride("q", q, shape, index)
-        q_out = k.new_empty(shape) if q_out is None else q_out
-        qo_ld = _row_stride("q_out", q_out, shape, index)
+        q_out, qo_ld = _output("q_out", q_out, shape, index, q, stream)
         q_at, qo_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -232,15 +244,13 @@ def hstu_paged_attn_fwd(q, k_cache, v_cache, page_table, q_offsets, kv_len, num_
     in the paged cache, the new ones included; the last num_targets of them are candidates.  Returns
     ``out``.  See include/hstu_paged.h."""
     load_library()
-    total, H, d, index = _first("q", q)
-    shape = (total, H, d)
-    q_ld = _row_stride("q", q, shape, index)
+    shape, q_ld, index = _first("q", q)
+    total, H, d = shape
     B = _users(q_offsets)
     off, lens = _index("q_offsets", q_offsets, B + 1, index), _index("kv_len", kv_len, B, index)
     targets = 0 if num_targets is None else _index("num_targets", num_targets, B, index)
     cache = _cache(k_cache, v_cache, page_table, B, H, d, index)
-    out = q.new_empty(shape) if out is None else out
-    out_ld = _row_stride("out", out, shape, index)
+    out, out_ld = _output("out", out, shape, index, q, stream)
     _call("hstu_paged_attn_fwd", index, stream, q.data_ptr(), q_ld, cache, off, lens, targets, B, H, d, total, max_new,
           max_kv, alpha, N, out.data_ptr(), out_ld)
     return out

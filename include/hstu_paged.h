@@ -23,6 +23,8 @@
  * New rows.  User b brings rows [q_offsets[b], q_offsets[b+1]) of the packed new-token tensors,
  * n_b of them; kv_len[b] is its length with them, so new row r is at position
  * kv_len[b] - n_b + r of its history.  n_b = 0 is legal, and so is a user with no earlier rows.
+ * Inconsistent offsets or lengths (see each call) are reported as HSTU_ERR_BAD_OFFSETS and the user is
+ * skipped; behind an offset that is smaller than the one before it, other users may be skipped too.
  */
 #ifndef HSTU_PAGED_H_
 #define HSTU_PAGED_H_

@@ -178,9 +178,9 @@ def test_no_targets_argument_strides_and_guard_rows(new):
     assert torch.all(big[0] == 7.0) and torch.all(big[-1] == 7.0) and torch.all(big[:, 0] == 7.0)
 
 
-@pytest.mark.parametrize("new", [4, 200])
-def test_deterministic_replayed_and_on_another_stream(new):
-    x = Batch([(600, new, 3), (2222, new, new // 2), (0, new, 1)], 32, 4, 128, seed=6)
+@pytest.mark.parametrize("new,long", [(4, 2222), (4, 23000), (200, 2222)])
+def test_deterministic_replayed_and_on_another_stream(new, long):
+    x = Batch([(600, new, 3), (long, new, new // 2), (0, new, 1)], 32, 4 if long < 9000 else 1, 128, seed=6)
     want = x.run()
     x.check(want)
     for _ in range(5):
@@ -212,6 +212,31 @@ def test_deterministic_replayed_and_on_another_stream(new):
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], again)
+
+
+@pytest.mark.parametrize("new", [3, 40, 100])
+def test_a_user_does_not_see_its_neighbours_rows(new):
+    """q, K and V of one user are NaN: the others' outputs are what they were, bit for bit."""
+    x = Batch([(77, new, 1), (130, new, 2), (40, new, 0)], 16, 2, 64, seed=12)
+    want = x.run()
+    x.check(want)
+    x.q[x.starts[1]:x.starts[2]] = float("nan")
+    x.pool.put(1, 0, *(torch.full_like(a, float("inf")) for a in x.kv[1]))
+    got = x.run()
+    assert torch.equal(got[:x.starts[1]], want[:x.starts[1]]) and torch.equal(got[x.starts[2]:], want[x.starts[2]:])
+
+
+@pytest.mark.parametrize("new", [3, 40, 100])
+def test_decreasing_offsets(new):
+    """Offsets that step back: reported; the users before the step are computed, nothing else is touched
+    beyond the rows the offsets name."""
+    x = Batch([(50, new, 1)] * 4, 16, 2, 64, seed=13)
+    off = dev_i32([0, new, 3 * new, 2 * new, 4 * new])
+    big = torch.full((4 * new + 8, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    x.run(off=off, out=big[4:-4])
+    assert binding.hstu_attn_get_error() == 4
+    x.check(big[4:-4], only=[0])
+    assert torch.all(big[:4] == 5.0) and torch.all(big[-4:] == 5.0)
 
 
 @pytest.mark.parametrize("new", [2, 90])

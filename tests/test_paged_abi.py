@@ -111,7 +111,7 @@ def _append(lib, cache=None, rot=None, **kw):
 
 
 def test_append_refusals(lib):
-    assert _append(lib, total=0) == OK and _append(lib, B=0) == OK
+    assert _append(lib, total=0) == OK and _append(lib, total=0, B=0) == OK and _append(lib, B=0) == INVALID
     for kw in (dict(k=None), dict(v=None), dict(off=None), dict(kv=None), dict(B=-1), dict(H=0), dict(total=-1), dict(k_ld=120),
                dict(q=1 << 24, q_ld=128, qo=1 << 25, qo_ld=128), dict(q=1 << 24, q_ld=128), dict(k=1 << 30),
                dict(v=(1 << 31) + 4096)):
@@ -139,7 +139,7 @@ def _attn(lib, cache=None, **kw):
 
 
 def test_attn_refusals(lib):
-    assert _attn(lib, total=0) == OK and _attn(lib, B=0) == OK
+    assert _attn(lib, total=0) == OK and _attn(lib, total=0, B=0) == OK and _attn(lib, B=0) == INVALID
     for kw in (dict(q=None), dict(out=None), dict(off=None), dict(kv=None), dict(B=-1), dict(H=0), dict(total=-1),
                dict(max_new=-1), dict(max_kv=-1), dict(alpha=float("nan")), dict(alpha=float("inf")), dict(N=0.0),
                dict(N=float("inf")), dict(q_ld=64), dict(out_ld=100), dict(out=1 << 20), dict(out=1 << 30),
