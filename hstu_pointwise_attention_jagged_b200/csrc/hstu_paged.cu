@@ -209,17 +209,17 @@ RowsShape rows_shape(const RowsArgs& a, int keys, int num_sms) {
   return s;
 }
 
-// A few rows a user.
-template <int D>
+// A few rows a user; R: rows of an item at most.
+template <int D, int R>
 hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t stream) {
   using Cfg = RowsCfg<D>;
   static std::once_flag once[kMaxDevices];
   static cudaError_t ready[kMaxDevices];
   cudaError_t e = once_per_device(once, ready, [] {
-    cudaError_t r = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t r = cudaFuncSetAttribute(paged_rows_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_rows_kernel<D, R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (r == cudaSuccess)
-      r = cudaFuncSetAttribute(paged_rows_run_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+      r = cudaFuncSetAttribute(paged_rows_run_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
     return r;
   });
   if (e != cudaSuccess) return HSTU_ERR_CUDA;
@@ -227,7 +227,7 @@ hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t
   const int64_t items = static_cast<int64_t>(a.B) * a.H * a.blocks;
   if (shape.clustered) {
     if (items * shape.cluster > INT_MAX) return HSTU_ERR_UNSUPPORTED;
-    e = launch_dependent(paged_rows_kernel<D>, items * shape.cluster, kRowsThreads, Cfg::kSmemBytes, shape.cluster, stream,
+    e = launch_dependent(paged_rows_kernel<D, R>, items * shape.cluster, kRowsThreads, Cfg::kSmemBytes, shape.cluster, stream,
                          a);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
@@ -241,7 +241,7 @@ hstu_status_t launch_rows(const RowsArgs& a, const DeviceState& st, cudaStream_t
   r.rows = a;
   r.parts = static_cast<int2*>(buf);
   r.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + parts_bytes);
-  e = launch_dependent(paged_rows_run_kernel<D>, runs, kRowsThreads, Cfg::kSmemBytes, 0, stream, r);
+  e = launch_dependent(paged_rows_run_kernel<D, R>, runs, kRowsThreads, Cfg::kSmemBytes, 0, stream, r);
   if (e == cudaSuccess) e = launch_dependent(paged_rows_sum_kernel<D>, items, kSumThreads, 0, 0, stream, r);
   if (cudaFreeAsync(buf, stream) != cudaSuccess && e == cudaSuccess) return HSTU_ERR_CUDA;
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
@@ -480,7 +480,11 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
   if (!rows_shape(a, 64 * 128 / d, st->num_sms).few)
     return d == 128 ? launch_many<128>(a, *cache, alpha, *st, cs)
                     : (d == 64 ? launch_many<64>(a, *cache, alpha, *st, cs) : launch_many<32>(a, *cache, alpha, *st, cs));
-  return d == 128 ? launch_rows<128>(a, *st, cs) : (d == 64 ? launch_rows<64>(a, *st, cs) : launch_rows<32>(a, *st, cs));
+  if (most <= 8)
+    return d == 128 ? launch_rows<128, 8>(a, *st, cs)
+                    : (d == 64 ? launch_rows<64, 8>(a, *st, cs) : launch_rows<32, 8>(a, *st, cs));
+  return d == 128 ? launch_rows<128, 16>(a, *st, cs)
+                  : (d == 64 ? launch_rows<64, 16>(a, *st, cs) : launch_rows<32, 16>(a, *st, cs));
 }
 
 }  // extern "C"

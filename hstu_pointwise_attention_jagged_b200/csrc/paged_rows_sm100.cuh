@@ -96,6 +96,12 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "r"(addr)
                : "memory");
 }
+// The transpose of an 8 x 8 matrix of 16-bit values held as one ldmatrix fragment.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 // c += a (16 x 16) * b (16 x 8), bf16 in, fp32 sums.
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -159,15 +165,30 @@ struct RowsCopy {
   }
 };
 
-// One item's query rows as this thread holds them: the A operand (rows lane / 4 and + 8, columns
-// 2 (lane % 4) + {0, 1, 8, 9} of each 16), and what each row sees: keys [0, lim) and `self`.
+// The arithmetic of one item in one warp: its query rows, what each of them sees, and O.  R rows at most,
+// 16 or 8: the product takes the R rows as its 16 rows, or, transposed (S' = K Q', O' = V' P'), as its
+// 8 columns, which halves the products, the SiLU and the registers of a call for up to 8 rows.
+//   visible: keys [0, lim) and `self`; U: history length, p0: position of row 0.
+template <int D, int R>
+struct RowsMath;
+
+// h = alpha s / 2 -> silu(alpha s) = h + h tanh(h); an invisible pair is selected to zero.
+__device__ __forceinline__ float rows_silu(float s, float half_alpha, bool visible) {
+  const float h = s * half_alpha;
+  const float p = fmaf(h, ptx::tanh_approx(h), h);
+  return visible ? p : 0.0f;
+}
+
 template <int D>
-struct RowsQuery {
-  uint32_t qf[D / 16][4];
-  int lim[2], self[2];
+struct RowsMath<D, 16> {
+  using Cfg = RowsCfg<D>;
+  static constexpr int kAcc = D / 8;
+  uint32_t qf[D / 16][4];  // rows lane / 4 (+ 8), columns 2 (lane % 4) + {0, 1, 8, 9} of each 16
+  float o[kAcc][4];        // [j]: rows lane / 4 (+ 8), columns 8 j + 2 (lane % 4) + {0, 1}
+  int lim[2], self[2];     // rows lane / 4 and + 8
   int U, p0;
 
-  __device__ __forceinline__ void load(const __nv_bfloat16* q, int64_t q_ld, int nrows, int first_pos, int hist) {
+  __device__ __forceinline__ void open(const __nv_bfloat16* q, int64_t q_ld, int nrows, int first_pos, int hist) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c2 = (lane & 3) * 2;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
@@ -183,63 +204,139 @@ struct RowsQuery {
       self[e] = p0 + g + e * 8;
       lim[e] = self[e] < U ? self[e] + 1 : U;
     }
+#pragma unroll
+    for (int j = 0; j < kAcc; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+  }
+
+  // O += P V for this warp's quarter of the tile whose first key is j0 and whose buffer is at `buf`.
+  __device__ __forceinline__ void tile(int j0, uint32_t buf, float half_alpha) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c2 = (lane & 3) * 2;
+    const int m = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row this lane addresses
+    const uint32_t sk = buf, sv = buf + Cfg::kTileBytes;
+    const bool full = j0 + Cfg::kKeys <= U && j0 + Cfg::kKeys <= p0 + 1;
+#pragma unroll
+    for (int kb = 0; kb < Cfg::kWarpKeys / 16; ++kb) {
+      const int key0 = warp * Cfg::kWarpKeys + kb * 16;  // first of this step's 16 keys in the tile
+      float s[2][4] = {};
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t kf[4];
+        ptx::ldmatrix4(kf, sk + Cfg::at(key0 + (m >> 1) * 8 + mr, ks * 2 + (m & 1)));
+        ptx::mma_16816(s[0], qf[ks], kf[0], kf[1]);
+        ptx::mma_16816(s[1], qf[ks], kf[2], kf[3]);
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + key0 + n * 8 + c2 + (e & 1);
+          s[n][e] = rows_silu(s[n][e], half_alpha, full || j < lim[e >> 1] || j == self[e >> 1]);
+        }
+      const uint32_t pf[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
+                              pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
+#pragma unroll
+      for (int jn = 0; jn < D / 16; ++jn) {
+        uint32_t vf[4];
+        ptx::ldmatrix4_trans(vf, sv + Cfg::at(key0 + (m & 1) * 8 + mr, jn * 2 + (m >> 1)));
+        ptx::mma_16816(o[2 * jn], pf, vf[0], vf[1]);
+        ptx::mma_16816(o[2 * jn + 1], pf, vf[2], vf[3]);
+      }
+    }
+  }
+
+  // f(row, column, x, y): two neighbouring columns, twice, of the four values that lane `lane` holds as o[j].
+  template <typename F>
+  __device__ static __forceinline__ void each(int j, int lane, float4 v, F&& f) {
+    const int r = lane >> 2, c = j * 8 + (lane & 3) * 2;
+    f(r, c, v.x, v.y);
+    f(r + 8, c, v.z, v.w);
   }
 };
 
-// O += P V for this warp's quarter of the tile whose first key is j0 and whose buffer is at `buf`.
 template <int D>
-__device__ __forceinline__ void rows_tile(float (&o)[D / 8][4], const RowsQuery<D>& q, int j0, uint32_t buf,
-                                          float half_alpha) {
+struct RowsMath<D, 8> {
   using Cfg = RowsCfg<D>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c2 = (lane & 3) * 2;
-  const int m = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row this lane addresses
-  const uint32_t sk = buf, sv = buf + Cfg::kTileBytes;
-  const bool full = j0 + Cfg::kKeys <= q.U && j0 + Cfg::kKeys <= q.p0 + 1;
+  static constexpr int kAcc = D / 16;
+  uint32_t qf[D / 16][2];  // row lane / 4, columns 2 (lane % 4) + {0, 1} and + 8 of each 16
+  float o[kAcc][4];        // [j]: columns 16 j + lane / 4 (+ 8 in the second pair), rows 2 (lane % 4) + {0, 1}
+  int lim[2], self[2];     // rows 2 (lane % 4) and + 1
+  int U, p0;
+
+  __device__ __forceinline__ void open(const __nv_bfloat16* q, int64_t q_ld, int nrows, int first_pos, int hist) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c2 = (lane & 3) * 2;
 #pragma unroll
-  for (int kb = 0; kb < Cfg::kWarpKeys / 16; ++kb) {
-    const int key0 = warp * Cfg::kWarpKeys + kb * 16;  // first of this step's 16 keys in the tile
-    float s[2][4] = {};
+    for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t kf[4];
-      const int r = key0 + (m >> 1) * 8 + mr;
-      ptx::ldmatrix4(kf, sk + Cfg::at(r, ks * 2 + (m & 1)));
-      ptx::mma_16816(s[0], q.qf[ks], kf[0], kf[1]);
-      ptx::mma_16816(s[1], q.qf[ks], kf[2], kf[3]);
+      for (int e = 0; e < 2; ++e)
+        qf[ks][e] = g < nrows ? *reinterpret_cast<const uint32_t*>(q + g * q_ld + c2 + ks * 16 + e * 8) : 0u;
+    U = hist;
+    p0 = first_pos;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      self[e] = p0 + c2 + e;
+      lim[e] = self[e] < U ? self[e] + 1 : U;
     }
-    // p = silu(alpha s) = hx + hx tanh(hx), hx = alpha s / 2; masked pairs select zero.
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int j = 0; j < kAcc; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+  }
+
+  __device__ __forceinline__ void tile(int j0, uint32_t buf, float half_alpha) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2;
+    const int m = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row this lane addresses
+    const uint32_t sk = buf, sv = buf + Cfg::kTileBytes;
+    const bool full = j0 + Cfg::kKeys <= U && j0 + Cfg::kKeys <= p0 + 1;
+#pragma unroll
+    for (int kb = 0; kb < Cfg::kWarpKeys / 16; ++kb) {
+      const int key0 = warp * Cfg::kWarpKeys + kb * 16;  // first of this step's 16 keys in the tile
+      // S': keys lane / 4 (+ 8), rows 2 (lane % 4) + {0, 1}; two chains of products, added.
+      float s[2][4] = {};
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t kf[4];
+        ptx::ldmatrix4(kf, sk + Cfg::at(key0 + (m & 1) * 8 + mr, ks * 2 + (m >> 1)));
+        ptx::mma_16816(s[ks & 1], kf, qf[ks][0], qf[ks][1]);
+      }
+      float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float hx = s[n][e] * half_alpha;
-        float v = fmaf(hx, ptx::tanh_approx(hx), hx);
-        if (!full) {
-          const int j = j0 + key0 + n * 8 + c2 + (e & 1);
-          v = (j < q.lim[e >> 1] || j == q.self[e >> 1]) ? v : 0.0f;
-        }
-        s[n][e] = v;
+        const int j = j0 + key0 + g + (e >> 1) * 8;
+        p[e] = rows_silu(s[0][e] + s[1][e], half_alpha, full || j < lim[e & 1] || j == self[e & 1]);
       }
-    const uint32_t pf[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                            pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
+      // P' as the 16 x 8 operand: keys 2 (lane % 4) + {0, 1} (+ 8), row lane / 4.
+      const uint32_t p0f = ptx::transpose_8x8(pack_bf16x2(p[0], p[1]));
+      const uint32_t p1f = ptx::transpose_8x8(pack_bf16x2(p[2], p[3]));
 #pragma unroll
-    for (int jn = 0; jn < D / 16; ++jn) {
-      uint32_t vf[4];
-      const int r = key0 + (m & 1) * 8 + mr;
-      ptx::ldmatrix4_trans(vf, sv + Cfg::at(r, jn * 2 + (m >> 1)));
-      ptx::mma_16816(o[2 * jn], pf, vf[0], vf[1]);
-      ptx::mma_16816(o[2 * jn + 1], pf, vf[2], vf[3]);
+      for (int jn = 0; jn < D / 16; ++jn) {
+        uint32_t vf[4];
+        ptx::ldmatrix4_trans(vf, sv + Cfg::at(key0 + (m >> 1) * 8 + mr, jn * 2 + (m & 1)));
+        ptx::mma_16816(o[jn], vf, p0f, p1f);
+      }
     }
   }
-}
 
-template <int D>
-__device__ __forceinline__ void rows_clear(float (&o)[D / 8][4]) {
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+  template <typename F>
+  __device__ static __forceinline__ void each(int j, int lane, float4 v, F&& f) {
+    const int c = j * 16 + (lane >> 2), r = (lane & 3) * 2;
+    f(r, c, v.x);
+    f(r + 1, c, v.y);
+    f(r, c + 8, v.z);
+    f(r + 1, c + 8, v.w);
+  }
+};
+
+__device__ __forceinline__ void rows_put(float* to, float x) { *to = x; }
+__device__ __forceinline__ void rows_put(float* to, float x, float y) {
+  *reinterpret_cast<float2*>(to) = make_float2(x, y);
+}
+__device__ __forceinline__ void rows_put(__nv_bfloat16* to, float x) { *to = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void rows_put(__nv_bfloat16* to, float x, float y) {
+  *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(x, y);
 }
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
@@ -256,9 +353,10 @@ __device__ __forceinline__ void rows_store(const RowsArgs& p, int row, int h, in
 // ---------------------------------------------------------------------------------------------
 // One cluster for each item
 // ---------------------------------------------------------------------------------------------
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsArgs p) {
   using Cfg = RowsCfg<D>;
+  using Math = RowsMath<D, R>;
   extern __shared__ __align__(128) uint8_t rows_smem[];
   const uint32_t sbase = ptx::smem_addr(rows_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -297,32 +395,28 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsA
   };
 #pragma unroll
   for (int s = 0; s < kRowsStages - 1; ++s) fetch(t_begin + s, s);
-  RowsQuery<D> q;
-  q.load(p.q + (int64_t)row0 * p.q_ld + (int64_t)h * D, p.q_ld, nrows, pos0, u.L - u.T);
-  float o[D / 8][4];
-  rows_clear<D>(o);
+  Math math;
+  math.open(p.q + (int64_t)row0 * p.q_ld + (int64_t)h * D, p.q_ld, nrows, pos0, u.L - u.T);
 
   int stage = 0;
   for (int t = t_begin; t < t_end; ++t) {
     ptx::cp_async_wait<kRowsStages - 2>();
     __syncthreads();
     fetch(t + kRowsStages - 1, stage == 0 ? kRowsStages - 1 : stage - 1);  // consumed in the previous step
-    rows_tile<D>(o, q, key_of(t), sbase + stage * Cfg::kStageBytes, p.half_alpha);
+    math.tile(key_of(t), sbase + stage * Cfg::kStageBytes, p.half_alpha);
     stage = stage + 1 == kRowsStages ? 0 : stage + 1;
   }
 
   // The four warps' sums, then the cluster's.
   ptx::cp_async_wait<0>();
   __syncthreads();
-  float* part = reinterpret_cast<float*>(rows_smem);  // [4][16][kPitch]
-  constexpr int kPitch = D + 8, kQuads = kPitch / 4;  // neighbouring rows in different banks
-  const int g = lane >> 2, c2 = (lane & 3) * 2;
+  float* part = reinterpret_cast<float*>(rows_smem);  // [4][R][kPitch]
+  constexpr int kPitch = D + (R == 16 ? 8 : 4), kQuads = kPitch / 4;  // a warp's stores hit 32 banks
+  float* mine = part + warp * R * kPitch;
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
-    float* at = part + (warp * kRowsBlock + g) * kPitch + j * 8 + c2;
-    *reinterpret_cast<float2*>(at) = make_float2(o[j][0], o[j][1]);
-    *reinterpret_cast<float2*>(at + 8 * kPitch) = make_float2(o[j][2], o[j][3]);
-  }
+  for (int j = 0; j < Math::kAcc; ++j)
+    Math::each(j, lane, make_float4(math.o[j][0], math.o[j][1], math.o[j][2], math.o[j][3]),
+               [&](int r, int c, auto... v) { rows_put(mine + r * kPitch + c, v...); });
   __syncthreads();
   const int quads = nrows * (D / 4);
   for (int i = tid; i < quads; i += kRowsThreads) {
@@ -330,7 +424,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_kernel(const RowsA
     float4* at = reinterpret_cast<float4*>(part) + r * kQuads + c;
     float4 a = *at;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) a = add4(a, at[w * kRowsBlock * kQuads]);
+    for (int w = 1; w < 4; ++w) a = add4(a, at[w * R * kQuads]);
     if (S > 1) *at = a;
     else rows_store<D>(p, row0 + r, h, c, a);
   }
@@ -370,9 +464,10 @@ struct RunsArgs {
   float* sums;
 };
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_run_kernel(const RunsArgs a) {
   using Cfg = RowsCfg<D>;
+  using Math = RowsMath<D, R>;
   const RowsArgs& p = a.rows;
   extern __shared__ __align__(128) uint8_t rows_smem[];
   const uint32_t sbase = ptx::smem_addr(rows_smem);
@@ -469,23 +564,21 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_run_kernel(const R
   };
 #pragma unroll
   for (int s = 0; s < kRowsStages - 1; ++s) fetch(s);
-  RowsQuery<D> q;
-  float o[D / 8][4];
+  Math math;
   bool fresh = true;
   int first_t = 0;  // the item's tile that this CTA began with
   int stage = 0;
   for (int x = x0; x < x1; ++x) {
     if (fresh) {
-      q.load(p.q + (int64_t)eat.u.q0 * p.q_ld + (int64_t)eat.h * D, p.q_ld, eat.u.n, eat.u.L - eat.u.n,
-             eat.u.L - eat.u.T);
-      rows_clear<D>(o);
+      math.open(p.q + (int64_t)eat.u.q0 * p.q_ld + (int64_t)eat.h * D, p.q_ld, eat.u.n, eat.u.L - eat.u.n,
+                eat.u.L - eat.u.T);
       fresh = false;
       first_t = eat.t;
     }
     ptx::cp_async_wait<kRowsStages - 2>();
     __syncthreads();
     fetch(stage == 0 ? kRowsStages - 1 : stage - 1);
-    rows_tile<D>(o, q, key_of(eat), sbase + stage * Cfg::kStageBytes, p.half_alpha);
+    math.tile(key_of(eat), sbase + stage * Cfg::kStageBytes, p.half_alpha);
     const bool last = eat.t + 1 == eat.n;
     if (last || x + 1 == x1) {
       // The end of the item or of the run: the warps' sums meet in the tile's buffer, which is free until
@@ -493,25 +586,21 @@ __global__ void __launch_bounds__(kRowsThreads, 2) paged_rows_run_kernel(const R
       float4* red = reinterpret_cast<float4*>(rows_smem + stage * Cfg::kStageBytes);
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        red[(warp * (D / 8) + j) * 32 + lane] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      for (int j = 0; j < Math::kAcc; ++j)
+        red[(warp * Math::kAcc + j) * 32 + lane] = make_float4(math.o[j][0], math.o[j][1], math.o[j][2], math.o[j][3]);
       __syncthreads();
       const bool head = first_t == 0, whole = head && last;
       float* slot = a.sums + (size_t)(2 * run + (head ? 1 : 0)) * kRowsBlock * D;
-      for (int i = tid; i < D / 8 * 32; i += kRowsThreads) {
+      __nv_bfloat16* out = p.out + (int64_t)eat.u.q0 * p.out_ld + (int64_t)eat.h * D;
+      for (int i = tid; i < Math::kAcc * 32; i += kRowsThreads) {
         float4 v = red[i];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) v = add4(v, red[w * (D / 8) * 32 + i]);
-        const int r = (i & 31) >> 2, c = (i >> 5) * 8 + (i & 3) * 2;  // rows r and r + 8, columns c and c + 1
-        __nv_bfloat16* out = p.out + (int64_t)(eat.u.q0 + r) * p.out_ld + (int64_t)eat.h * D + c;
-        if (r < eat.u.n) {
-          if (whole) *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(v.x * p.inv_n, v.y * p.inv_n);
-          else *reinterpret_cast<float2*>(slot + r * D + c) = make_float2(v.x, v.y);
-        }
-        if (r + 8 < eat.u.n) {
-          if (whole) *reinterpret_cast<uint32_t*>(out + 8 * p.out_ld) = pack_bf16x2(v.z * p.inv_n, v.w * p.inv_n);
-          else *reinterpret_cast<float2*>(slot + (r + 8) * D + c) = make_float2(v.z, v.w);
-        }
+        for (int w = 1; w < 4; ++w) v = add4(v, red[w * Math::kAcc * 32 + i]);
+        Math::each(i >> 5, i & 31, v, [&](int r, int c, auto... x) {
+          if (r >= eat.u.n) return;
+          if (whole) rows_put(out + r * p.out_ld + c, x * p.inv_n...);
+          else rows_put(slot + r * D + c, x...);
+        });
       }
       if (head && tid == 0)
         a.parts[(int64_t)eat.b * p.H + eat.h] = make_int2(run, run_of(tiles, runs, x + eat.n - 1 - eat.t));
