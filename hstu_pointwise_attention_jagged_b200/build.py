@@ -1,7 +1,9 @@
-"""Builds ``libhstu_attn.so`` (the CUDA library behind include/hstu_attn.h and include/hstu_paged.h) in-tree for sm_100a."""
+"""Builds, in-tree, ``libhstu_attn.so`` (the CUDA library behind include/hstu_attn.h and include/hstu_paged.h,
+for sm_100a) and ``_paged_native.so`` (the C++ marshalling of the paged calls for Python)."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -12,24 +14,54 @@ SOURCES = ["hstu_attn.cu", "hstu_paged.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I" + INCLUDE, "-I" + CSRC]
+MODULE = os.path.join(PKG, "_paged_native.so")
+MODULE_SOURCES = ["paged_binding.cpp"]
+CXX = os.environ.get("CXX", "g++")
 
 
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f not in MODULE_SOURCES]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, inputs) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in inputs)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _inputs())
+
+
+def build_module(force: bool = False) -> str:
+    """Compiles the marshalling module if a source of it is newer; returns its path."""
+    sources = [os.path.join(CSRC, s) for s in MODULE_SOURCES]
+    if not force and _newer(MODULE, sources + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] +
+                            [os.path.abspath(__file__)]):
+        return MODULE
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = MODULE + ".tmp%d" % os.getpid()
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I" + INCLUDE, "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-o", tmp] + sources + ["-L" + os.path.join(home, "lib")] + [
+           "-l" + lib for lib in ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda")]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MODULE)
+    return MODULE
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles the library if any source is newer than it; returns the library path."""
+    """Compiles what is older than its sources; returns the library's path."""
+    build_module(force)
     if not force and up_to_date():
         return LIB
     tmp = LIB + ".tmp%d" % os.getpid()

@@ -45,17 +45,21 @@ def test_exports(lib):
         assert re.search(r"\sT %s$" % name, out, re.M), name
 
 
-def test_packed_structs():
-    """The binding packs the two structs as bytes; the layout is the C compiler's."""
-    from hstu_pointwise_attention_jagged_b200 import paged
-    raw = paged._CACHE.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
-    c = PagedCache.from_buffer_copy(raw)
-    assert len(raw) == ctypes.sizeof(PagedCache)
-    assert [getattr(c, n) for n, _ in PagedCache._fields_] == list(range(1, 11))
-    raw = paged._ROTATION.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
-    r = Rotation.from_buffer_copy(raw)
-    assert len(raw) == ctypes.sizeof(Rotation)
-    assert [r.freqs, r.pairs, r.axes, *r.sections, r.interleaved, r.positions, r.positions_ld] == list(range(1, 11))
+def test_marshalling_refuses_without_a_gpu(lib):
+    """The checks come before any GPU work: CPU tensors, wrong types, unknown and missing arguments."""
+    import torch
+    from hstu_pointwise_attention_jagged_b200 import hstu_paged_append, hstu_paged_attn_fwd, hstu_rotary
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: hstu_rotary(x, None, i, torch.zeros(32, dtype=torch.float64)),
+                 lambda: hstu_rotary("q", None, i, i), lambda: hstu_rotary(x, None, i), lambda: hstu_rotary(),
+                 lambda: hstu_rotary(x, None, i, i, angle=3), lambda: hstu_rotary(x, None, i, i, q=x),
+                 lambda: hstu_rotary(*[x] * 11),
+                 lambda: hstu_paged_append(x, x, x, x, i, i, i), lambda: hstu_paged_append(x, x, x, x, i, kv_len=i),
+                 lambda: hstu_paged_attn_fwd(x, x, x, i, i, i, None, 1.0, 1.0, 4, 4),
+                 lambda: hstu_paged_attn_fwd(None, x, x, i, i, i, None, 1.0, 1.0, 4, 4)):
+        with pytest.raises(TypeError):
+            call()
 
 
 def _rotation(**kw):
