@@ -121,7 +121,7 @@ struct FwdParams {
   float inv_n;
   unsigned* err;
   uint64_t wait_limit_ns;      // limit of every pipeline wait (kWaitLimitNs; a self-check lowers it)
-  PagedFwd paged;              // paged form only; there q_start is q_offsets
+  PagedFwd paged;              // paged form only
 };
 
 template <int kStages>
@@ -375,7 +375,7 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
   uint32_t commit_par = 0u;          // g - kStages / 2's, and its phase (first waited for as group 1)
   bool loose = false;
   Source v0{}, v1{}, v2{};  // V tiles g-3, g-2, g-1
-  bool ok = true;
+  bool ok = true, first = true;
   auto copy = [&](const CUtensorMap* tm, uint32_t dst, uint32_t rb, const Source& s) {
     if (issues) ptx::tma_load_4d(dst + box_off, tm, rb, blk * Cfg::kBlockElems, s.row, s.h, s.page);
   };
@@ -431,25 +431,27 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
     Piece pc{};
     int b = 0;
     if (chief) {
-      int idx = 0;
-      if (lane == 0) idx = atomicAdd(p.work_counter, 1);
-      idx = __shfl_sync(0xffffffffu, idx, 0);
+      // The CTA's first piece is its own number's; the others come from the queue.
+      int idx = (int)blockIdx.x;
+      if (!first) {
+        if (lane == 0) idx = (int)gridDim.x + atomicAdd(p.work_counter, 1);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+      }
+      first = false;
       w.valid = idx < M;
       if (w.valid) {
         const int4* at = reinterpret_cast<const int4*>(plan.pieces + idx);
-        const int4 x = at[0], y = at[1];
-        const PagedPiece pp{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        if (pp.tiles == 0) continue;
-        b = pp.b;
-        pc = Piece{pp.tile0, pp.tiles, pp.parts, pp.part, pp.pitch};
-        const int q0 = p.q_start[b], n = p.q_start[b + 1] - q0;
-        w.h = pp.h;
-        w.kv_start = idx - pp.part * pp.pitch;
-        w.L = p.paged.kv_len[b];
-        w.U = w.L - (p.num_targets ? p.num_targets[b] : 0);
-        w.q_row0 = q0 + pp.block * kItemRows;
-        w.pos0 = w.L - n + pp.block * kItemRows;
-        w.nrows = min(n - pp.block * kItemRows, kItemRows);
+        const int4 x = at[0], y = at[1], z = at[2];
+        if (z.x == 0) continue;
+        b = x.x;
+        w.h = x.y;
+        w.q_row0 = x.z;
+        w.pos0 = x.w;
+        w.nrows = y.x;
+        w.L = y.y;
+        w.U = y.z;
+        pc = Piece{y.w, z.x, z.y, z.z, z.w};
+        w.kv_start = idx - pc.part * pc.pitch;
       }
       if (!wait_all(bar(ctl->sched_empty[slot]), (sched_par >> slot) & 1u)) {
         ok = false;
@@ -1032,8 +1034,9 @@ __global__ void __launch_bounds__(kPaged ? kPagedThreads : kNumThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, Cfg::kTmemCols);
-  // The last CTA to finish re-arms the plan's work counter, so the same plan can be replayed.
-  if (threadIdx.x == 0) {
+  // The last CTA to finish re-arms the plan's work counter, so the same plan can be replayed.  (A paged
+  // call makes its own plan.)
+  if (!kPaged && threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(p.done_counter, 1) == (int)gridDim.x - 1) {
       atomicExch(p.work_counter, 0);

@@ -314,11 +314,8 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   s.total_new = a.total_new;
   s.max_new = a.max_new;
   s.max_kv = a.max_kv;
-  s.nbins = cost_bins(a.max_kv);
   s.wave_rows = plan_wave_rows(a.H);
-  s.nwaves = plan_waves(static_cast<int64_t>(a.B) * a.max_kv, s.wave_rows, s.nbins);
   s.num_ctas = ctas;
-  s.max_items = static_cast<int32_t>(capacity);
   s.max_cut = static_cast<int32_t>(max_cut);
   s.plan.header = reinterpret_cast<int32_t*>(at);
   s.plan.block_start = reinterpret_cast<int32_t*>(at + o_block);
@@ -327,10 +324,7 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   s.err = a.err;
   FwdParams p;
   std::memset(&p, 0, sizeof(p));
-  p.num_targets = a.num_targets;
-  p.q_start = a.q_offsets;
   p.work_counter = s.plan.header;
-  p.done_counter = s.plan.header + 2;
   p.out = a.out;
   p.out_ld = a.out_ld;
   p.H = a.H;
@@ -339,7 +333,6 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   p.err = a.err;
   p.wait_limit_ns = kWaitLimitNs;
   p.paged.cache = a.cache;
-  p.paged.kv_len = a.kv_len;
   p.paged.plan = s.plan;
   p.paged.partials = reinterpret_cast<float4*>(at + o_partials);
   e = launch_dependent(paged_schedule_kernel, 1, kSchedThreads, 0, 0, stream, s);

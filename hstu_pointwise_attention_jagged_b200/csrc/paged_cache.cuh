@@ -41,16 +41,19 @@ __device__ __forceinline__ PagedUser paged_user(const PagedView& c, const int32_
   return u;
 }
 
+// A piece of work of the many-row attention: key tiles [tile0, tile0 + tiles) of an item's (user b, head h,
+// `nrows` query rows from row q_row0 of q, at positions pos0 on of a user with L rows, U of them
+// history).  tiles = 0: nothing to do.
 struct PagedPiece {
-  int32_t b, block, h;
-  int32_t tile0, tiles;  // tiles [tile0, tile0 + tiles) of the item's; tiles = 0: nothing to do
-  int32_t parts, part;   // pieces of the item (1: whole) and which one this is
-  int32_t pitch;         // queue places between the item's pieces
+  int32_t b, h, q_row0, pos0;
+  int32_t nrows, L, U, tile0;
+  int32_t tiles, parts, part, pitch;  // parts: pieces of the item (1: whole); part: which one this is;
+                                      // pitch: queue places between the item's pieces
 };
-static_assert(sizeof(PagedPiece) == 32, "two 16-byte loads");
+static_assert(sizeof(PagedPiece) == 48, "three 16-byte loads");
 
 struct PagedPlan {
-  int32_t* header;       // [8] {queue counter, pieces, finished CTAs, cuts, 0, 0, 0, 0}
+  int32_t* header;       // [4] {pieces taken beyond the CTAs' first ones, pieces, 0, 0}
   int32_t* block_start;  // [B+1] first block of each user
   int32_t* done;         // [4 * max_cut] finished pieces of a cut item, for each quarter of its rows
   PagedPiece* pieces;    // [max_pieces] the queue
@@ -59,7 +62,6 @@ struct PagedPlan {
 // The paged form of the forward kernel's parameters.
 struct PagedFwd {
   PagedView cache;
-  const int32_t* kv_len;
   PagedPlan plan;
   float4* partials;  // [queue place][D / 4][128 rows]: fp32 sums of the pieces of cut items
 };

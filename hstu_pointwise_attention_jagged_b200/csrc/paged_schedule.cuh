@@ -8,6 +8,10 @@
 // estimate rounds * (q + overhead).  The pieces of a cut item leave fp32 partial outputs, and the last one to
 // finish adds them up in order (hstu_fwd_sm100.cuh, epilogue).  Pieces of one key range of one user and head
 // are neighbours in the queue: CTAs that work side by side read the same K and V.
+//
+// The plan is one CTA's work between two kernels, so what it costs is latency, much of it fetching
+// instructions that run once: loops are not unrolled, the block scan is one function, 64-bit divisions are
+// avoided, and each block's cost is computed once and kept on chip.
 #pragma once
 
 #include <climits>
@@ -21,113 +25,179 @@ namespace hstu {
 constexpr int kMaxCutRounds = 4;  // cut items make at most this many pieces for each CTA
 constexpr int kMaxCuts = 16;      // pieces of the longest item
 constexpr int kMinPieceTiles = 2;
-constexpr int kPieceOverhead = 3; // tiles: filling the pipeline, writing and adding the partial
+constexpr int kPieceOverhead = 3; // tiles: filling the pipeline, writing and adding the partial (measured)
+constexpr int kCachedBlocks = 2048;  // batches up to this many 128-row blocks keep their costs in shared memory
 
 struct PagedSchedArgs {
   PagedView cache;
   const int32_t* q_offsets;
   const int32_t* kv_len;
   const int32_t* num_targets;
-  int32_t B, H, total_new, max_new, max_kv, nbins, nwaves, wave_rows, num_ctas, max_items, max_cut;  // max_items: H * (total_new / 128 + B)
+  int32_t B, H, total_new, max_new, max_kv, wave_rows, num_ctas, max_cut;
   PagedPlan plan;
   unsigned* err;
 };
 
+// Inclusive prefix sum over the CTA of one value a thread; *total gets the sum.  scratch: kSchedWarps values.
+static __device__ __noinline__ int paged_scan(int v, int* scratch, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < kSchedWarps; ++w) {
+    if (w < warp) v += scratch[w];
+    sum += scratch[w];
+  }
+  *total = sum;
+  __syncthreads();
+  return v;
+}
+
+// Block g of a user: its rows and tiles.
+__device__ __forceinline__ int block_rows(const PagedUser& u, int blk) { return min(u.n - blk * kItemRows, kItemRows); }
+__device__ __forceinline__ int block_cost(const PagedUser& u, int blk) {
+  return item_cost(u.L - u.n + blk * kItemRows, block_rows(u, blk), u.L - u.T);
+}
+
 // One CTA of kSchedThreads threads.
 __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const PagedSchedArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int hist[kMaxCostBins];
-  __shared__ long long scan_scratch[2][32];
-  __shared__ long long carry_blocks, carry_rows;
+  __shared__ __align__(16) int hist[kMaxCostBins];
+  __shared__ int scratch[kSchedWarps];
+  __shared__ int carry_blocks, carry_tiles;
   __shared__ int first_bad;  // first user whose offsets decrease
   __shared__ int longest, pieces_of[kMaxCuts + 1];
   __shared__ PagedUser s_user[kCachedUsers];
-  __shared__ int s_start[kCachedUsers + 1], s_wave[kCachedUsers], s_cost[kCachedUsers];
-  const bool cached = a.B <= kCachedUsers;
+  __shared__ int s_start[kCachedUsers + 1], s_tiles[kCachedUsers], s_cost[kCachedUsers];
+  __shared__ unsigned s_block[kCachedBlocks];  // user | cost << 8
+  static_assert(kCachedUsers <= 256, "a user in 8 bits");
   const int tid = threadIdx.x;
   if (tid == 0) {
     carry_blocks = 0;
-    carry_rows = 0;
+    carry_tiles = 0;
     longest = 0;
     first_bad = INT_MAX;
   }
   if (tid <= kMaxCuts) pieces_of[tid] = 0;
+  for (int i = tid; i < kMaxCostBins / 4; i += kSchedThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  const bool few_users = a.B <= kCachedUsers;
+  auto user = [&](int b) {
+    return paged_user(a.cache, a.q_offsets, a.kv_len, a.num_targets, b, a.total_new, a.max_new, a.max_kv);
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
 
-  // Pass 1: check every user; prefix sums of 128-row blocks and of cached rows.
+  // Pass 1: check every user; prefix sums of 128-row blocks and, for the waves, of 128-row key tiles.
+#pragma unroll 1
   for (int base = 0; base < a.B; base += kSchedThreads) {
     const int b = base + tid;
-    long long blocks = 0, rows = 0;
+    int blocks = 0, tiles = 0;
     PagedUser u;
     if (b < a.B) {
-      u = paged_user(a.cache, a.q_offsets, a.kv_len, a.num_targets, b, a.total_new, a.max_new, a.max_kv);
-      bool bad = !u.ok;
-      if (b == 0) bad |= u.q0 != 0;
-      if (b == a.B - 1) bad |= a.q_offsets[a.B] != a.total_new;
-      if (bad) atomicOr(a.err, kErrBadOffsets);
-      if (a.q_offsets[b + 1] < u.q0) atomicMin(&first_bad, b);
+      u = user(b);
+      const int next = a.q_offsets[b + 1];
+      if (!u.ok || (b == 0 && u.q0 != 0) || (b == a.B - 1 && next != a.total_new)) atomicOr(a.err, kErrBadOffsets);
+      if (next < u.q0) atomicMin(&first_bad, b);
     }
     __syncthreads();
     if (b < a.B) {
       // Behind decreasing offsets users may overlap, and their blocks be more than the plan has room for.
       if (!u.ok || b >= first_bad) u.n = u.L = 0;
       blocks = cdiv(u.n, kItemRows);
-      rows = u.n > 0 ? u.L : 0;
+      tiles = u.n > 0 ? min(u.L / kTileRows, 1 << 22) : 0;  // the sum of 256 fits
     }
-    long long incl_b = blocks, incl_r = rows, tot_b, tot_r;
-    block_inclusive_scan2(incl_b, incl_r, scan_scratch, tot_b, tot_r);
+    int all_blocks, all_tiles = 0;
+    const int start = carry_blocks + paged_scan(blocks, scratch, &all_blocks) - blocks;
+    const int before = few_users ? carry_tiles + paged_scan(tiles, scratch, &all_tiles) - tiles : 0;
     if (b < a.B) {
-      const int start = (int)(carry_blocks + incl_b - blocks);
-      const long long wave = (carry_rows + incl_r - rows) / a.wave_rows;
       a.plan.block_start[b] = start;
-      if (cached) {
+      if (few_users) {
         s_user[b] = u;
         s_start[b] = start;
-        s_wave[b] = (int)(wave < a.nwaves ? wave : a.nwaves - 1);
+        s_tiles[b] = before;
         s_cost[b] = 0;
       }
     }
     __syncthreads();
     if (tid == 0) {
-      carry_blocks += tot_b;
-      carry_rows += tot_r;
+      carry_blocks += all_blocks;
+      carry_tiles += all_tiles;
     }
     __syncthreads();
   }
-  const int nblocks = (int)carry_blocks;
+  const int nblocks = carry_blocks;  // times H: at most the plan's room, H * (total_new / 128 + B)
   if (tid == 0) {
     a.plan.block_start[a.B] = nblocks;
-    if (cached) s_start[a.B] = nblocks;
+    if (few_users) s_start[a.B] = nblocks;
   }
   __syncthreads();
-  const int items = nblocks * a.H;  // at most a.max_items
-  // Block g: its user, index within the user and tiles.
-  auto block_of = [&](int g, int& b, int& blk) {
-    b = owner_of(cached ? s_start : a.plan.block_start, a.B, g);
-    blk = g - (cached ? s_start[b] : a.plan.block_start[b]);
-    const PagedUser u = cached ? s_user[b]
-                               : paged_user(a.cache, a.q_offsets, a.kv_len, a.num_targets, b, a.total_new, a.max_new,
-                                            a.max_kv);
-    const int rows = u.n - blk * kItemRows;
-    return item_cost(u.L - u.n + blk * kItemRows, rows < kItemRows ? rows : kItemRows, u.L - u.T);
+
+  // Pass 2: every block's tiles.
+  const bool cached = few_users && nblocks <= kCachedBlocks;
+  auto start_of = [&](int b) { return few_users ? s_start[b] : a.plan.block_start[b]; };
+  auto owner = [&](int g) { return few_users ? owner_of(s_start, a.B, g) : owner_of(a.plan.block_start, a.B, g); };
+  auto known = [&](int b) { return few_users ? s_user[b] : user(b); };
+  int most_tiles = 0;
+#pragma unroll 1
+  for (int g = tid; g < nblocks; g += kSchedThreads) {
+    const int b = owner(g), cost = block_cost(known(b), g - start_of(b));
+    most_tiles = max(most_tiles, cost);
+    if (cached) {
+      s_block[g] = (unsigned)b | (unsigned)cost << 8;
+      atomicMax(&s_cost[b], cost);
+    }
+  }
+  most_tiles = __reduce_max_sync(0xffffffffu, most_tiles);
+  if ((tid & 31) == 0) atomicMax(&longest, most_tiles);
+  __syncthreads();
+  const int top = longest;
+  auto block_of = [&](int g, int& b, int& blk, int& cost) {
+    if (cached) {
+      b = (int)(s_block[g] & 255u);
+      cost = (int)(s_block[g] >> 8);
+    } else {
+      b = owner(g);
+      cost = -1;
+    }
+    blk = g - start_of(b);
+    if (cost < 0) cost = block_cost(known(b), blk);
+  };
+  auto piece_of = [&](int b, int blk, int cost) {
+    const PagedUser u = known(b);
+    PagedPiece p;
+    p.b = b;
+    p.q_row0 = u.q0 + blk * kItemRows;
+    p.pos0 = u.L - u.n + blk * kItemRows;
+    p.nrows = block_rows(u, blk);
+    p.L = u.L;
+    p.U = u.L - u.T;
+    p.tile0 = 0;
+    p.tiles = cost;
+    p.parts = 1;
+    p.part = p.pitch = 0;
+    return p;
+  };
+  auto put = [&](int at, const PagedPiece& p) {
+    int4* to = reinterpret_cast<int4*>(a.plan.pieces + at);
+    to[0] = make_int4(p.b, p.h, p.q_row0, p.pos0);
+    to[1] = make_int4(p.nrows, p.L, p.U, p.tile0);
+    to[2] = make_int4(p.tiles, p.parts, p.part, p.pitch);
   };
 
   // Cuts that can be tried: c pieces of every item may not be more than there is room for.
+  const int items = nblocks * a.H;
   const int most = items > 0 ? min(kMaxCuts, a.max_cut / items) : 1;
   if (cached && most > 1) {
-    // Most tiles of an item, for each user (s_cost) and in all.
-    for (int g = tid; g < nblocks; g += kSchedThreads) {
-      int b, blk;
-      const int cost = block_of(g, b, blk);
-      atomicMax(&s_cost[b], cost);
-      atomicMax(&longest, cost);
-    }
-    __syncthreads();
     // Pieces when the longest item is cut in c.
-    const int top = longest;
     if (tid < a.B && s_cost[tid] > 0) {
       const int rows = (s_start[tid + 1] - s_start[tid]) * a.H;
+#pragma unroll 1
       for (int c = 1; c <= most; ++c) atomicAdd(&pieces_of[c], rows * cdiv(s_cost[tid], cdiv(top, c)));
     }
     __syncthreads();
@@ -138,97 +208,86 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
       if (best == 1 || q >= kMinPieceTiles)
         time = cdiv(pieces_of[best], a.num_ctas) * (q + (best > 1 ? kPieceOverhead : 0));
     }
-    for (int o = 16; o > 0; o >>= 1) {
-      const int t2 = __shfl_xor_sync(0xffffffffu, time, o), b2 = __shfl_xor_sync(0xffffffffu, best, o);
-      if (t2 < time || (t2 == time && b2 < best)) {
-        time = t2;
-        best = b2;
-      }
-    }
+    const int least = __reduce_min_sync(0xffffffffu, time);
+    best = __reduce_min_sync(0xffffffffu, time == least ? best : INT_MAX);
     if (best > 1) {
       // Queue places: user, head, part, block.  Every item of a user is cut alike; the places of parts
       // that a short item does not have stay empty.
       const int q = cdiv(top, best);
-      long long mine = 0, tot;
-      if (tid < a.B) mine = (long long)(s_start[tid + 1] - s_start[tid]) * a.H * cdiv(s_cost[tid], q);
-      const int first = (int)(block_inclusive_scan(mine, scan_scratch[0], &tot) - mine);
-      if (tid < a.B) hist[tid] = first;
+      const int mine = tid < a.B ? (s_start[tid + 1] - s_start[tid]) * a.H * cdiv(s_cost[tid], q) : 0;
+      int total;
+      const int first = paged_scan(mine, scratch, &total) - mine;
+      if (tid < a.B) s_tiles[tid] = first;
       __syncthreads();
-      for (int x = tid; x < nblocks * a.H; x += kSchedThreads) {
-        PagedPiece p;
-        p.h = x / nblocks;
-        const int cost = block_of(x - p.h * nblocks, p.b, p.block);
-        const int parts = cdiv(s_cost[p.b], q);
-        p.pitch = s_start[p.b + 1] - s_start[p.b];
+#pragma unroll 1
+      for (int x = tid; x < items; x += kSchedThreads) {
+        const int h = x / nblocks;
+        int b, blk, cost;
+        block_of(x - h * nblocks, b, blk, cost);
+        PagedPiece p = piece_of(b, blk, cost);
+        p.h = h;
+        const int parts = cdiv(s_cost[b], q);
+        p.pitch = s_start[b + 1] - s_start[b];
         p.parts = min(parts, cost);
-        const int at = hist[p.b] + p.h * parts * p.pitch + p.block;
+        const int at = s_tiles[b] + h * parts * p.pitch + blk;
+#pragma unroll 1
         for (p.part = 0; p.part < parts; ++p.part) {
           p.tile0 = p.part < p.parts ? cost * p.part / p.parts : 0;
           p.tiles = p.part < p.parts ? cost * (p.part + 1) / p.parts - p.tile0 : 0;
-          a.plan.pieces[at + p.part * p.pitch] = p;
+          put(at + p.part * p.pitch, p);
         }
-        for (int k = 0; k < 4; ++k) a.plan.done[at * 4 + k] = 0;
+        reinterpret_cast<int4*>(a.plan.done)[at] = make_int4(0, 0, 0, 0);
       }
-      if (tid == 0) {
-        a.plan.header[0] = 0;
-        a.plan.header[1] = (int)tot;
-        a.plan.header[2] = 0;
-        a.plan.header[3] = best;
-      }
+      if (tid == 0) *reinterpret_cast<int4*>(a.plan.header) = make_int4(0, total, 0, 0);
       return;
     }
   }
 
-  // Whole items, as schedule_kernel: a counting sort of the blocks by (wave, non-increasing cost).
-  const long long waves = (carry_rows + a.wave_rows - 1) / a.wave_rows;  // that the batch reaches
-  const int nkeys = a.nbins * (int)(cached && waves < a.nwaves ? (waves > 0 ? waves : 1) : a.nwaves);
-  for (int i = tid; i < nkeys; i += kSchedThreads) hist[i] = 0;
-  __syncthreads();
+  // Whole items: a counting sort of the blocks by (wave, non-increasing cost).  Waves are those the batch
+  // reaches, or fewer that hold more; costs are rounded to bins that fit the key space.
+  const int wave_tiles = max(1, a.wave_rows / kTileRows);
+  int shift = 0;
+  while ((top >> shift) >= kMaxCostBins / 2) ++shift;
+  const int bins = (top >> shift) + 1;
+  const int waves = min(few_users ? carry_tiles / wave_tiles + 1 : 16, kMaxCostBins / bins);
+  const int nkeys = bins * waves;
   auto key_of = [&](int b, int cost) {
-    int wave = 0;
-    if (cached) wave = s_wave[b];
-    else wave = (int)((int64_t)b * a.nwaves / a.B);  // large batches: by the user's index
-    return wave * a.nbins + (a.nbins - 1 - (cost < a.nbins ? cost : a.nbins - 1));
+    const int wave = few_users ? min(s_tiles[b] / wave_tiles, waves - 1) : (int)((int64_t)b * waves / a.B);
+    return wave * bins + ((top - cost) >> shift);
   };
+#pragma unroll 1
   for (int g = tid; g < nblocks; g += kSchedThreads) {
-    int b, blk;
-    const int cost = block_of(g, b, blk);
+    int b, blk, cost;
+    block_of(g, b, blk, cost);
     atomicAdd(&hist[key_of(b, cost)], a.H);
   }
   __syncthreads();
   const int per = cdiv(nkeys, kSchedThreads);
-  long long part = 0;
+  int part = 0, total;
+#pragma unroll 1
   for (int k = 0; k < per; ++k)
     if (tid * per + k < nkeys) part += hist[tid * per + k];
-  __syncthreads();
-  long long tot;
-  long long run = block_inclusive_scan(part, scan_scratch[0], &tot) - part;
+  int run = paged_scan(part, scratch, &total) - part;
+#pragma unroll 1
   for (int k = 0; k < per; ++k) {
     const int key = tid * per + k;
     if (key < nkeys) {
       const int n = hist[key];
-      hist[key] = (int)run;
+      hist[key] = run;
       run += n;
     }
   }
   __syncthreads();
+#pragma unroll 1
   for (int g = tid; g < nblocks; g += kSchedThreads) {
-    PagedPiece p;
-    const int cost = block_of(g, p.b, p.block);
-    p.tile0 = 0;
-    p.tiles = cost;
-    p.parts = 1;
-    p.part = p.pitch = 0;
-    const int pos = atomicAdd(&hist[key_of(p.b, cost)], a.H);
-    for (p.h = 0; p.h < a.H; ++p.h)
-      if (pos + p.h < items) a.plan.pieces[pos + p.h] = p;
+    int b, blk, cost;
+    block_of(g, b, blk, cost);
+    PagedPiece p = piece_of(b, blk, cost);
+    const int at = atomicAdd(&hist[key_of(b, cost)], a.H);
+#pragma unroll 1
+    for (p.h = 0; p.h < a.H; ++p.h) put(at + p.h, p);
   }
-  if (tid == 0) {
-    a.plan.header[0] = 0;
-    a.plan.header[1] = items;
-    a.plan.header[2] = 0;
-    a.plan.header[3] = 1;
-  }
+  if (tid == 0) *reinterpret_cast<int4*>(a.plan.header) = make_int4(0, items, 0, 0);
 }
 
 }  // namespace hstu
