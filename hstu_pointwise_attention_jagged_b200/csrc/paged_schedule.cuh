@@ -38,17 +38,19 @@ struct PagedSchedArgs {
   unsigned* err;
 };
 
-// Inclusive prefix sum over the CTA of one value a thread; *total gets the sum.  scratch: kSchedWarps values.
-static __device__ __noinline__ int paged_scan(int v, int* scratch, int* total) {
+// Inclusive prefix sum over the CTA of one value a thread (or two, in the halves of 64 bits); *total gets
+// the sum.  scratch: kSchedWarps values.
+template <typename T>
+static __device__ __noinline__ T paged_scan(T v, T* scratch, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, v, o);
+    const T n = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += n;
   }
   if (lane == 31) scratch[warp] = v;
   __syncthreads();
-  int sum = 0;
+  T sum = 0;
 #pragma unroll
   for (int w = 0; w < kSchedWarps; ++w) {
     if (w < warp) v += scratch[w];
@@ -69,8 +71,8 @@ __device__ __forceinline__ int block_cost(const PagedUser& u, int blk) {
 __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const PagedSchedArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ __align__(16) int hist[kMaxCostBins];
+  __shared__ unsigned long long scratch2[kSchedWarps];
   __shared__ int scratch[kSchedWarps];
-  __shared__ int carry_blocks, carry_tiles;
   __shared__ int first_bad;  // first user whose offsets decrease
   __shared__ int longest, pieces_of[kMaxCuts + 1];
   __shared__ PagedUser s_user[kCachedUsers];
@@ -79,12 +81,9 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   static_assert(kCachedUsers <= 256, "a user in 8 bits");
   const int tid = threadIdx.x;
   if (tid == 0) {
-    carry_blocks = 0;
-    carry_tiles = 0;
     longest = 0;
     first_bad = INT_MAX;
   }
-  if (tid <= kMaxCuts) pieces_of[tid] = 0;
   for (int i = tid; i < kMaxCostBins / 4; i += kSchedThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   const bool few_users = a.B <= kCachedUsers;
   auto user = [&](int b) {
@@ -93,11 +92,12 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
 
-  // Pass 1: check every user; prefix sums of 128-row blocks and, for the waves, of 128-row key tiles.
+  // Pass 1: check every user; prefix sums of 128-row blocks (low half) and, for the waves, of key tiles.
+  unsigned long long carry = 0;
 #pragma unroll 1
   for (int base = 0; base < a.B; base += kSchedThreads) {
     const int b = base + tid;
-    int blocks = 0, tiles = 0;
+    unsigned long long mine = 0;
     PagedUser u;
     if (b < a.B) {
       u = user(b);
@@ -109,29 +109,24 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     if (b < a.B) {
       // Behind decreasing offsets users may overlap, and their blocks be more than the plan has room for.
       if (!u.ok || b >= first_bad) u.n = u.L = 0;
-      blocks = cdiv(u.n, kItemRows);
-      tiles = u.n > 0 ? min(u.L / kTileRows, 1 << 22) : 0;  // the sum of 256 fits
+      const int tiles = u.n > 0 ? min(u.L / kTileRows, 1 << 22) : 0;  // the sum of kCachedUsers fits 31 bits
+      mine = (unsigned)cdiv(u.n, kItemRows) | (unsigned long long)tiles << 32;
     }
-    int all_blocks, all_tiles = 0;
-    const int start = carry_blocks + paged_scan(blocks, scratch, &all_blocks) - blocks;
-    const int before = few_users ? carry_tiles + paged_scan(tiles, scratch, &all_tiles) - tiles : 0;
+    unsigned long long all;
+    const unsigned long long upto = carry + paged_scan(mine, scratch2, &all) - mine;
+    carry += all;
     if (b < a.B) {
+      const int start = (int)(unsigned)upto;
       a.plan.block_start[b] = start;
       if (few_users) {
         s_user[b] = u;
         s_start[b] = start;
-        s_tiles[b] = before;
+        s_tiles[b] = (int)(upto >> 32);
         s_cost[b] = 0;
       }
     }
-    __syncthreads();
-    if (tid == 0) {
-      carry_blocks += all_blocks;
-      carry_tiles += all_tiles;
-    }
-    __syncthreads();
   }
-  const int nblocks = carry_blocks;  // times H: at most the plan's room, H * (total_new / 128 + B)
+  const int nblocks = (int)(unsigned)carry;  // times H: at most the plan's room, H * (total_new / 128 + B)
   if (tid == 0) {
     a.plan.block_start[a.B] = nblocks;
     if (few_users) s_start[a.B] = nblocks;
@@ -192,22 +187,28 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
 
   // Cuts that can be tried: c pieces of every item may not be more than there is room for.
   const int items = nblocks * a.H;
-  const int most = items > 0 ? min(kMaxCuts, a.max_cut / items) : 1;
+  const int most = items > 0 ? min(min(kMaxCuts, top / kMinPieceTiles), a.max_cut / items) : 1;
   if (cached && most > 1) {
-    // Pieces when the longest item is cut in c.
-    if (tid < a.B && s_cost[tid] > 0) {
-      const int rows = (s_start[tid + 1] - s_start[tid]) * a.H;
+    // Pieces when the longest item is cut in c: kSchedThreads / kMaxCuts threads count the users for each c.
+    {
+      constexpr int kEach = kSchedThreads / kMaxCuts;
+      static_assert(kEach == 16, "a half warp each");
+      const int c = tid / kEach + 1;
+      int n = 0;
+      if (c <= most) {
+        const int q = cdiv(top, c);
 #pragma unroll 1
-      for (int c = 1; c <= most; ++c) atomicAdd(&pieces_of[c], rows * cdiv(s_cost[tid], cdiv(top, c)));
+        for (int b = tid % kEach; b < a.B; b += kEach) n += (s_start[b + 1] - s_start[b]) * a.H * cdiv(s_cost[b], q);
+      }
+#pragma unroll
+      for (int o = kEach / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (tid % kEach == 0) pieces_of[c] = n;
     }
     __syncthreads();
     // The best c by estimated time, ties to the smaller: lane c - 1 of each warp rates c.
     int best = (tid & 31) + 1, time = INT_MAX;
-    if (best <= most && best <= top && pieces_of[best] <= a.max_cut) {
-      const int q = cdiv(top, best);
-      if (best == 1 || q >= kMinPieceTiles)
-        time = cdiv(pieces_of[best], a.num_ctas) * (q + (best > 1 ? kPieceOverhead : 0));
-    }
+    if (best <= most && pieces_of[best] <= a.max_cut)
+      time = cdiv(pieces_of[best], a.num_ctas) * (cdiv(top, best) + (best > 1 ? kPieceOverhead : 0));
     const int least = __reduce_min_sync(0xffffffffu, time);
     best = __reduce_min_sync(0xffffffffu, time == least ? best : INT_MAX);
     if (best > 1) {
@@ -249,17 +250,30 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   int shift = 0;
   while ((top >> shift) >= kMaxCostBins / 2) ++shift;
   const int bins = (top >> shift) + 1;
-  const int waves = min(few_users ? carry_tiles / wave_tiles + 1 : 16, kMaxCostBins / bins);
+  const int waves = min(few_users ? (int)(carry >> 32) / wave_tiles + 1 : 16, kMaxCostBins / bins);
   const int nkeys = bins * waves;
   auto key_of = [&](int b, int cost) {
     const int wave = few_users ? min(s_tiles[b] / wave_tiles, waves - 1) : (int)((int64_t)b * waves / a.B);
     return wave * bins + ((top - cost) >> shift);
   };
+  // Lanes with the same key add to it together: equal costs are the rule.
+  auto claim = [&](int key, int& rank) {
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    rank = __popc(same & ((1u << (tid & 31)) - 1u));
+    const int leader = __ffs(same) - 1;
+    int at = 0;
+    if (key >= 0 && rank == 0) at = atomicAdd(&hist[key], __popc(same) * a.H);
+    return __shfl_sync(0xffffffffu, at, leader);
+  };
+  const int rounds = cdiv(nblocks, kSchedThreads);
 #pragma unroll 1
-  for (int g = tid; g < nblocks; g += kSchedThreads) {
-    int b, blk, cost;
-    block_of(g, b, blk, cost);
-    atomicAdd(&hist[key_of(b, cost)], a.H);
+  for (int k = 0; k < rounds; ++k) {
+    int b, blk, cost, rank, key = -1;
+    if (k * kSchedThreads + tid < nblocks) {
+      block_of(k * kSchedThreads + tid, b, blk, cost);
+      key = key_of(b, cost);
+    }
+    claim(key, rank);
   }
   __syncthreads();
   const int per = cdiv(nkeys, kSchedThreads);
@@ -279,13 +293,18 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   }
   __syncthreads();
 #pragma unroll 1
-  for (int g = tid; g < nblocks; g += kSchedThreads) {
-    int b, blk, cost;
-    block_of(g, b, blk, cost);
+  for (int k = 0; k < rounds; ++k) {
+    const bool there = k * kSchedThreads + tid < nblocks;
+    int b, blk, cost, rank, key = -1;
+    if (there) {
+      block_of(k * kSchedThreads + tid, b, blk, cost);
+      key = key_of(b, cost);
+    }
+    const int at = claim(key, rank);
+    if (!there) continue;
     PagedPiece p = piece_of(b, blk, cost);
-    const int at = atomicAdd(&hist[key_of(b, cost)], a.H);
 #pragma unroll 1
-    for (p.h = 0; p.h < a.H; ++p.h) put(at + p.h, p);
+    for (p.h = 0; p.h < a.H; ++p.h) put(at + rank * a.H + p.h, p);
   }
   if (tid == 0) *reinterpret_cast<int4*>(a.plan.header) = make_int4(0, items, 0, 0);
 }
