@@ -30,7 +30,6 @@ constexpr int kRotBatch = 2, kRotPasses = 2;
 constexpr int kRotSideRows = 16;    // rows side by side at most
 constexpr int kRotMaxRows = kRotSideRows * kRotBatch * kRotPasses;  // rows of a block
 constexpr int kRotMaxPairs = 64;
-constexpr int kRotScanUsers = 1024; // batches up to this size: each block scans the offsets for its rows' users
 
 enum RotTarget : int32_t { kToRows = 0, kToCacheK = 1, kToCacheV = 2 };
 
@@ -110,8 +109,8 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotArgs p)
   // (cos, sin) of row r, pair 8 u + 2 j + e at float2 index ((r * 4 + j) * (pairs / 8) + u) * 2 + e, so
   // that neighbouring units read neighbouring float4.
   extern __shared__ float4 s_cs[];
-  __shared__ int64_t s_dst[kRotMaxRows];            // element offset of the row in the cache, -1: not written
-  __shared__ unsigned long long s_key[kRotMaxRows]; // user << 32 | place of the row, ~0: no user's row
+  __shared__ int64_t s_dst[kRotMaxRows];    // element offset of the row in the cache, -1: not written
+  __shared__ int32_t s_place[kRotMaxRows];  // the row's place in its user's cache, -1: no user's row
   const int tid = threadIdx.x, threads = blockDim.x;
   const int row0 = blockIdx.x * p.block_rows;
   const int nrows = min(p.block_rows, p.rows - row0);
@@ -166,31 +165,47 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotArgs p)
     load_batch(u, side);
   }
 
+  auto angles = [&] {
+    // Thread -> pair tid % pairs of rows tid / pairs + k * (threads / pairs).
+    const int i = tid % pairs, step = threads / pairs;
+    if (tid >= step * pairs) return;
+    const int axis = (p.axes > 1 && i >= p.section_end[0]) + (p.axes > 2 && i >= p.section_end[1]) +
+                     (p.axes > 3 && i >= p.section_end[2]);
+    const uint64_t turns = turns_of(p.freqs[i]);
+    const int32_t* pos = p.positions ? p.positions + axis * p.positions_ld + row0 : nullptr;
+    float2* to = reinterpret_cast<float2*>(s_cs) + (((i >> 1) & 3) * (pairs >> 3) + (i >> 3)) * 2 + (i & 1);
+    for (int r = tid / pairs; r < nrows; r += step) {
+      const int at = pos ? pos[r] : s_place[r];
+      const int part = (int)(uint32_t)(((uint64_t)(int64_t)at * turns) >> 32);  // 2^-32 turns, signed
+      float sn, cs;
+      sincospif((float)part * 0x1p-31f, &sn, &cs);
+      to[r * pairs] = make_float2(cs, p.sign * sn);
+    }
+  };
+
   if constexpr (kPaged) {
-    // Whose rows these are.  Up to kRotScanUsers users every block looks at all offsets, which costs one
-    // round of coalesced loads; beyond that each row searches for itself.
-    auto claim = [&](int b, int lo, int hi) {
-      const PagedUser v = paged_user(p.cache, p.q_offsets, p.kv_len, nullptr, b, p.rows, INT_MAX, -1);
-      if (!v.ok) return;
-      for (int r = lo; r < hi; ++r)
-        atomicMin(&s_key[r], (unsigned long long)(unsigned)b << 32 | (unsigned)(v.L - v.n + (row0 + r - v.q0)));
-    };
-    if (tid < nrows) s_key[tid] = ~0ull;
-    __syncthreads();
-    if (p.B <= kRotScanUsers) {
-      for (int b = tid; b < p.B; b += threads) {
-        const int lo = max(p.q_offsets[b] - row0, 0), hi = min(p.q_offsets[b + 1] - row0, nrows);
-        if (lo < hi) claim(b, lo, hi);
+    // Whose row this is and where it goes: a thread for each row, kRotMaxRows at most and no more than there
+    // are threads.  The search's loads hit L1 after the SM's first block.
+    if (tid < nrows) {
+      const int row = row0 + tid;
+      int lo = 0, hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (p.q_offsets[mid] <= row) lo = mid; else hi = mid;
       }
-    } else {
-      for (int r = tid; r < nrows; r += threads) {
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-          const int mid = lo + (hi - lo) / 2;
-          if (p.q_offsets[mid] <= row0 + r) lo = mid; else hi = mid;
-        }
-        if (p.q_offsets[lo] <= row0 + r && row0 + r < p.q_offsets[lo + 1]) claim(lo, r, r + 1);
+      const PagedUser v = paged_user(p.cache, p.q_offsets, p.kv_len, nullptr, lo, p.rows, INT_MAX, -1);
+      int64_t dst = -1;
+      int place = -1;
+      if (v.ok && v.q0 <= row && row < v.q0 + v.n) {
+        place = v.L - v.n + (row - v.q0);
+        const int page = p.cache.table[lo * p.cache.table_ld + (place >> p.cache.page_shift)];
+        if (page >= 0 && page < p.cache.num_pages)
+          dst = page * p.cache.page_stride + (place & ((1 << p.cache.page_shift) - 1)) * p.cache.row_stride;
+        else
+          atomicOr(p.err, kErrBadOffsets);
       }
+      s_dst[tid] = dst;
+      s_place[tid] = place;
     }
     if (blockIdx.x == 0) {
       bool bad = tid == 0 && (p.q_offsets[0] != 0 || p.q_offsets[p.B] != p.rows);
@@ -198,39 +213,9 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotArgs p)
         bad |= !paged_user(p.cache, p.q_offsets, p.kv_len, nullptr, b, p.rows, INT_MAX, -1).ok;
       if (bad) atomicOr(p.err, kErrBadOffsets);
     }
-    __syncthreads();
-    for (int r = tid; r < nrows; r += threads) {
-      int64_t dst = -1;
-      if (s_key[r] != ~0ull) {
-        const int b = (int)(s_key[r] >> 32), place = (int)(s_key[r] & 0xffffffffu);
-        const int page = p.cache.table[b * p.cache.table_ld + (place >> p.cache.page_shift)];
-        if (page >= 0 && page < p.cache.num_pages)
-          dst = page * p.cache.page_stride + (place & ((1 << p.cache.page_shift) - 1)) * p.cache.row_stride;
-        else
-          atomicOr(p.err, kErrBadOffsets);
-      }
-      s_dst[r] = dst;
-    }
+    if (pairs > 0 && p.positions == nullptr) __syncthreads();  // the angles are of the places
   }
-
-  if (pairs > 0) {
-    // Thread -> pair tid % pairs of rows tid / pairs + k * (threads / pairs).
-    const int i = tid % pairs, step = threads / pairs;
-    if (tid < step * pairs) {
-      const int axis = (p.axes > 1 && i >= p.section_end[0]) + (p.axes > 2 && i >= p.section_end[1]) +
-                       (p.axes > 3 && i >= p.section_end[2]);
-      const uint64_t turns = turns_of(p.freqs[i]);
-      const int32_t* pos = p.positions ? p.positions + axis * p.positions_ld + row0 : nullptr;
-      float2* to = reinterpret_cast<float2*>(s_cs) + (((i >> 1) & 3) * (pairs >> 3) + (i >> 3)) * 2 + (i & 1);
-      for (int r = tid / pairs; r < nrows; r += step) {
-        const int at = pos ? pos[r] : (int)(s_key[r] & 0xffffffffu);
-        const int part = (int)(uint32_t)(((uint64_t)(int64_t)at * turns) >> 32);  // 2^-32 turns, signed
-        float sn, cs;
-        sincospif((float)part * 0x1p-31f, &sn, &cs);
-        to[r * pairs] = make_float2(cs, p.sign * sn);
-      }
-    }
-  }
+  if (pairs > 0) angles();
   __syncthreads();
   if (!active) return;
 
@@ -256,7 +241,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotArgs p)
           to = s_dst[r];
           if (to < 0) continue;
         } else {
-          if (kPaged && s_key[r] == ~0ull) continue;
+          if (kPaged && s_place[r] < 0) continue;
           to = r * t.dst_ld;
         }
         *reinterpret_cast<uint4*>(base + to + u.c0) = held[i].a;
