@@ -146,8 +146,8 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int thread
 }
 
 // Shape of the rotation's blocks: as many rows side by side as have a thread for each unit, and
-// kRotBatch x kRotPasses units for each thread; fewer rows where that would leave SMs without a block (a call for a few rows is
-// bound by the latency of one block).
+// kRotBatch x kRotPasses units for each thread; fewer rows where that would leave SMs without a block (a
+// call for a few rows is bound by the latency of one block).
 hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState& st, cudaStream_t stream) {
   a.head_shift = d == 128 ? 3 : (d == 64 ? 2 : 1);
   const int64_t units = static_cast<int64_t>(a.tensors) * a.H << a.head_shift;
@@ -159,7 +159,8 @@ hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState
   a.side_rows = at_most(a.side_rows, spread);
   a.block_rows = at_most(a.side_rows * kRotBatch * kRotPasses, spread);
   int threads = at_most((a.side_rows * units + 31) / 32 * 32, kRotThreads);
-  if (threads < 64) threads = 64;  // the angles: at least one thread a pair
+  if (threads < 64) threads = 64;  // the angles and the look-ups: at least one thread a pair, and one a row
+  static_assert(kRotMaxPairs <= 64 && kRotMaxRows <= 64, "threads of the smallest block");
   const int grid = (a.rows + a.block_rows - 1) / a.block_rows;
   const int smem = a.block_rows * a.pairs * 8;
   const cudaError_t e = paged ? launch_dependent(rotary_kernel<true>, grid, threads, smem, 0, stream, a)

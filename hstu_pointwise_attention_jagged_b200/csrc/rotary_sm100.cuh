@@ -24,8 +24,8 @@
 namespace hstu {
 
 constexpr int kRotThreads = 256;    // at most
-// Units a thread has in flight, and how often over (measured at 2 x 2, 4 x 1, 4 x 2, 2 x 1 and 1 x 4: rotation of
-// 32768 x 512 Q and K in 23.6, 25.5, 25.6, 26.2 and 26.7 us, streaming append 45.7, 49.3, 47.0, 54.6 and 45.8).
+// Units a thread has in flight, and how often over (measured at 2 x 2, 4 x 1, 2 x 4, 3 x 2 and 1 x 4: rotation of
+// 32768 x 512 Q and K in 23.7, 26.3, 24.0, 23.8 and 25.6 us, streaming append 42.1, 46.1, 45.2, 42.2 and 44.1).
 constexpr int kRotBatch = 2, kRotPasses = 2;
 constexpr int kRotSideRows = 16;    // rows side by side at most
 constexpr int kRotMaxRows = kRotSideRows * kRotBatch * kRotPasses;  // rows of a block

@@ -71,8 +71,8 @@ typedef struct hstu_paged_cache {
  * and the columns behind them pass unchanged.  With several axes (the place of an event in the
  * history, its time, ...) the pairs are shared out in runs: the first sections[0] pairs turn with
  * axis 0, the next sections[1] with axis 1, and so on.  Angles are reduced in 64 bits, so positions
- * may be Unix times: t is exact to about 1e-6 for |pos * freqs| up to 2^33 radians.
- *   freqs         device double [pairs], 8-byte aligned.
+ * may be Unix times: t is good to 1e-6 for |pos * freqs| up to 2^31 radians.
+ *   freqs         device double [pairs], finite, 8-byte aligned.
  *   pairs         a multiple of 8, 2 * pairs <= d.
  *   axes          1 .. HSTU_MAX_AXES; sections[0 .. axes) are >= 0 and add up to `pairs`.
  *   positions     device int32: axis a of row t at positions[a * positions_ld + t].

@@ -48,7 +48,7 @@ class Pool:
     """A page pool with every user's pages in random places; unused table entries are -1 or garbage.
 
     layout: "rows" [pages, P, H, d], "heads" [pages, H, P, d], "halves" K and V as the two halves of
-    [pages, 2, P, H, d]."""
+    [pages, 2, P, H, d], "padded" rows, heads and pages with gaps between them."""
 
     def __init__(self, lengths, page, H, d, layout="rows", seed=0, spare=3, fill=float("nan"), extra_width=2):
         rng = np.random.default_rng(seed)
@@ -71,6 +71,9 @@ class Pool:
         elif layout == "heads":
             self.k, self.v = (torch.full((self.pages, H, page, d), fill, dtype=torch.bfloat16, device="cuda")
                               .transpose(1, 2) for _ in range(2))
+        elif layout == "padded":
+            self.k, self.v = (torch.full((self.pages, page + 3, H + 1, d + 8), fill, dtype=torch.bfloat16,
+                                         device="cuda")[:, :page, :H, :d] for _ in range(2))
         else:
             both = torch.full((self.pages, 2, page, H, d), fill, dtype=torch.bfloat16, device="cuda")
             self.k, self.v = both[:, 0], both[:, 1]

@@ -17,6 +17,7 @@ CASES = [  # cached, new rows, page, H, d, layout
     ([0, 129, 64, 0, 7], [300, 0, 64, 0, 1000], 8, 3, 128, "halves"),
     ([10, 2000], [1500, 49], 1024, 2, 64, "rows"),
     ([17] * 40, list(range(40)), 128, 8, 32, "heads"),
+    ([9, 1, 70], [3, 60, 1], 32, 3, 128, "padded"),
 ]
 
 
@@ -138,6 +139,20 @@ def test_bad_users_and_pages_are_skipped_and_reported():
     off_bad[5] = 19
     paged.hstu_paged_append(k, v, pool.k, pool.v, pool.table, off_bad, kv)
     assert binding.hstu_attn_get_error() == 4
+
+
+def test_decreasing_offsets():
+    """Offsets that step back: reported; nothing but cache rows that the offsets and lengths name is written."""
+    cached, new = [20, 20, 20], [4, 4, 4]
+    pool, q, k, v, off, kv = _setup(cached, new, 8, 2, 64, "rows", 6)
+    at = [pool.where(b, 20, 24) for b in range(3)]
+    paged.hstu_paged_append(k, v, pool.k, pool.v, pool.table, dev_i32([0, 8, 4, 12]), kv)
+    assert binding.hstu_attn_get_error() == 4
+    for b in (1, 2):
+        pool.k[at[b]] = float("nan")
+    for idx in (pool.where(0, 16, 24), pool.where(2, 16, 24)):
+        pool.k[idx] = float("nan")
+    assert torch.isnan(pool.k).all()
 
 
 def test_capture_and_other_stream():

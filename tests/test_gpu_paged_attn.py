@@ -62,6 +62,7 @@ SMALL = [
     ([(300, 1, 0)] * 9, 32, 4, "heads"),
     ([(700, 4, 3), (0, 0, 0), (255, 16, 0), (256, 16, 16), (257, 13, 5)], 16, 3, "halves"),
     ([(2000, 1, 0), (3, 2, 1), (4100, 1, 1)], 128, 1, "rows"),
+    ([(100, 3, 1), (33, 1, 0)], 16, 3, "padded"),
     ([(1500, 7, 2), (90, 9, 9)], 1024, 2, "heads"),
 ]
 LARGE = [
@@ -72,6 +73,7 @@ LARGE = [
     ([(0, 128, 128), (384, 127, 3), (640, 200, 100)], 64, 3, "heads"),
     ([(900, 600, 500), (0, 64, 0)], 256, 1, "halves"),
     ([(1300, 40, 0)], 8, 4, "rows"),
+    ([(1000, 300, 40), (77, 130, 0)], 32, 2, "padded"),
     ([(250, 33, 20)] * 30, 32, 2, "rows"),
     ([(100, 1100, 1000)], 1024, 2, "heads"),
 ]
