@@ -192,8 +192,10 @@ struct RowsShape {
 // 18.2 against 24.0; 16 x 4 of 3000, 12 tiles, 20.3 against 24.2; 64 x 4 of ragged histories up to 4096,
 // 64 tiles, 62 against 41; 1 x 4 of 32000, 31 tiles, 29 against 20.)
 //
-// Users of 17 to 64 rows go here while the call is short; otherwise every block of 16 rows reading all
-// keys costs more than the tcgen05 kernel's plan and fill.
+// More than 16 rows a user come here while the call is short.  Every block of 16 rows reads all keys again,
+// but the tcgen05 kernel has its plan, its fill and tiles of 128 rows to pay for.  (us, here against there:
+// 4 users x 4 heads of 100 rows over 1000, d = 128, 13.1 against 18.0; 1 x 4 of 256 over 2000, 13.7 against
+// 24.9; 16 x 4 of 80 over 300, 14.5 against 13.6; 64 x 4 of 24 over 300, 17.6 against 21.0.)
 RowsShape rows_shape(const RowsArgs& a, int keys, int num_sms) {
   const int64_t items = static_cast<int64_t>(a.B) * a.H * a.blocks;
   const int64_t tiles = a.max_kv / keys + 1;  // of an item, at most
@@ -204,7 +206,7 @@ RowsShape rows_shape(const RowsArgs& a, int keys, int num_sms) {
   s.clustered = stretch <= kRowsClusterTiles || a.B > kRunUsers || items * tiles > INT_MAX;
   s.few = a.blocks == 1;
   if (a.blocks > 1) {
-    s.few = a.max_new <= kRowsMaxNew && stretch <= kRowsBlocksTiles && items * tiles <= 2 * num_sms * kRowsBlocksTiles;
+    s.few = stretch <= kRowsClusterTiles && items * tiles <= 2 * num_sms * kRowsBlocksTiles;
     s.clustered = true;
   }
   return s;

@@ -17,7 +17,7 @@
 //   paged_rows_kernel      one cluster of CTAs for each item; the partial O's are added over distributed
 //                          shared memory, in rank order.  One launch and no workspace: for calls whose
 //                          time is latency, and for batches of so many items that each needs one CTA.
-//                          Up to 64 rows a user become several items if the call stays short.
+//                          More than 16 rows a user become several items while the call stays short.
 //   paged_rows_run_kernel  the tiles of all items, in item order, dealt out in equal runs to two CTAs for
 //                          each SM; parts of items go to a workspace and paged_rows_sum_kernel adds them in
 //                          order.  Ragged lengths and any number of items load every SM alike.
@@ -36,11 +36,10 @@ namespace hstu {
 
 constexpr int kRowsThreads = 128;
 constexpr int kRowsBlock = 16;        // query rows of a CTA
-constexpr int kRowsMaxNew = 64;       // rows of a user at most
 constexpr int kRowsStages = 3;
 constexpr int kRowsMaxSplit = 16;     // CTAs of a cluster
-constexpr int kRowsClusterTiles = 16; // tiles of a CTA of a cluster at most, for one block of rows a user
-constexpr int kRowsBlocksTiles = 8;   // ... and for several
+constexpr int kRowsClusterTiles = 16; // tiles of a CTA of a cluster at most
+constexpr int kRowsBlocksTiles = 12;  // with several blocks a user: tiles in all, for each CTA the GPU holds
 
 template <int D>
 struct RowsCfg {

@@ -15,10 +15,13 @@ from paged_util import Pool, bf16_normal, dense64, offsets_of
 pytestmark = pytest.mark.gpu
 
 
-class Batch:
-    """users: (cached rows, new rows, candidates among them)."""
+LONG = 1 << 20  # a bound on the lengths that makes more than 16 rows a user take the tcgen05 kernel
 
-    def __init__(self, users, page, H, d, layout="rows", seed=1, scale=1.0, alpha=None):
+
+class Batch:
+    """users: (cached rows, new rows, candidates among them).  bound: max_kv, if not the longest length."""
+
+    def __init__(self, users, page, H, d, layout="rows", seed=1, scale=1.0, alpha=None, bound=None):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         self.users, self.H, self.d = users, H, d
         lengths = [c + n for c, n, _ in users]
@@ -32,7 +35,7 @@ class Batch:
         self.off, self.kv_len = offsets_of(new), dev_i32(lengths)
         self.nt = dev_i32([t for _, _, t in users])
         self.alpha, self.N = 1 / math.sqrt(d) if alpha is None else alpha, float(max(lengths + [1]))
-        self.max_new, self.max_kv = max(new + [0]), max(lengths + [0])
+        self.max_new, self.max_kv = max(new + [0]), bound or max(lengths + [0])
         self.starts = np.concatenate([[0], np.cumsum(new)])
 
     def run(self, **kw):
@@ -95,7 +98,7 @@ def test_many_rows(case, d):
     users, page, H, layout = LARGE[case]
     x = Batch(users, page, H, d, layout, seed=case + 11)
     x.check(x.run())
-    x.check(x.run(max_new=5000, max_kv=9000))  # bounds that rule out the few-rows form
+    x.check(x.run(max_new=5000, max_kv=LONG))
     assert binding.hstu_attn_get_error() == 0
 
 
@@ -108,15 +111,15 @@ def test_many_users_of_few_rows(users):
     x = Batch([(int(c), int(n), int(rng.integers(0, n + 1))) for c, n in zip(cached, new)], 16, 1, 32, seed=users)
     x.check(x.run(), only=set(rng.choice(users, 200).tolist()) | {0, users - 1})
     assert binding.hstu_attn_get_error() == 0
-    big = [(int(c), int(n), 0) for c, n in zip(cached, 20 * new)]  # the same through the many-row kernel
-    x = Batch(big, 16, 1, 32, seed=users + 1)
+    big = [(int(c), int(n), 0) for c, n in zip(cached, 20 * new)]  # the same through the tcgen05 kernel
+    x = Batch(big, 16, 1, 32, seed=users + 1, bound=LONG)
     x.check(x.run(), only=set(rng.choice(users, 200).tolist()) | {0, users - 1})
 
 
 @pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256, 512, 1024])
-@pytest.mark.parametrize("new", [3, 150])
-def test_page_sizes(page, new):
-    x = Batch([(page - 1, new, 1), (page, new, 0), (2 * page + 5, new, new)], page, 2, 64, "rows", seed=page)
+@pytest.mark.parametrize("new,bound", [(3, None), (150, None), (150, LONG)])
+def test_page_sizes(page, new, bound):
+    x = Batch([(page - 1, new, 1), (page, new, 0), (2 * page + 5, new, new)], page, 2, 64, "rows", seed=page, bound=bound)
     x.check(x.run())
 
 
@@ -126,6 +129,7 @@ def test_bounds_larger_than_the_batch(new):
     x = Batch([(200, new, 5), (0, new, 0), (77, 1, 0)], 16, 2, 64, "rows", seed=new)
     x.check(x.run())
     x.check(x.run(max_new=4 * new, max_kv=20000))
+    x.check(x.run(max_new=4 * new, max_kv=LONG))
 
 
 @pytest.mark.parametrize("users", [[(5000, 1, 0), (40, 1, 1)], [(5000, 200, 100), (40, 60, 1)]])
@@ -133,9 +137,11 @@ def test_large_scores_and_alpha(users):
     """Scores of size 30 (SiLU near 0 and near x), a negative alpha, and alpha = 0."""
     x = Batch(users, 16, 1, 64, scale=3.0, alpha=0.5, seed=3)
     x.check(x.run())
+    x.check(x.run(max_kv=LONG))
     for alpha in (-0.25, 0.0):
         x = Batch(users, 16, 1, 64, alpha=alpha, seed=4)
         x.check(x.run())
+        x.check(x.run(max_kv=LONG))
 
 
 @pytest.mark.parametrize("users,H,d,page", [([(33000, 2, 1)], 1, 128, 16), ([(20000, 1, 0), (12000, 16, 8)], 2, 64, 64),
@@ -151,22 +157,22 @@ def test_long_users(users, H, d, page):
     assert_parity(out, want, what="paged long d=%d" % d, users=np.repeat(np.arange(len(users)), [n for _, n, _ in users]))
 
 
-@pytest.mark.parametrize("new", [2, 140])
-def test_equals_the_contiguous_call(new):
+@pytest.mark.parametrize("new,bound", [(2, None), (140, None), (140, LONG)])
+def test_equals_the_contiguous_call(new, bound):
     """The same batch through hstu_attn_fwd_cached: within both calls' error bound of fp64."""
     users = [(321, new, 1), (0, new, 0), (1000, new, new)]
-    x = Batch(users, 16, 4, 128, seed=21)
+    x = Batch(users, 16, 4, 128, seed=21, bound=bound)
     out = x.run()
     x.check(out)
     k, v = (torch.cat([a[i] for a in x.kv]) for i in (0, 1))
     seq = offsets_of([c + n for c, n, _ in users])
-    x.check(binding.hstu_attn_fwd_cached(x.q, k, v, seq, x.nt, dev_i32([c for c, _, _ in users]), x.alpha, x.N, x.max_kv))
+    x.check(binding.hstu_attn_fwd_cached(x.q, k, v, seq, x.nt, dev_i32([c for c, _, _ in users]), x.alpha, x.N, int(x.kv_len.max())))
 
 
-@pytest.mark.parametrize("new", [3, 60])
-def test_no_targets_argument_strides_and_guard_rows(new):
+@pytest.mark.parametrize("new,bound", [(3, None), (60, None), (60, LONG)])
+def test_no_targets_argument_strides_and_guard_rows(new, bound):
     users = [(100, new, 0), (0, 0, 0), (17, new, 0)]
-    x = Batch(users, 16, 2, 64, seed=5)
+    x = Batch(users, 16, 2, 64, seed=5, bound=bound)
     want = x.run()
     x.check(want)
     assert torch.equal(x.run(nt=None), want)
@@ -180,9 +186,10 @@ def test_no_targets_argument_strides_and_guard_rows(new):
     assert torch.all(big[0] == 7.0) and torch.all(big[-1] == 7.0) and torch.all(big[:, 0] == 7.0)
 
 
-@pytest.mark.parametrize("new,long", [(4, 2222), (4, 23000), (200, 2222)])
-def test_deterministic_replayed_and_on_another_stream(new, long):
-    x = Batch([(600, new, 3), (long, new, new // 2), (0, new, 1)], 32, 4 if long < 9000 else 1, 128, seed=6)
+@pytest.mark.parametrize("new,long,bound", [(4, 2222, None), (4, 23000, None), (200, 2222, None), (200, 2222, LONG),
+                                            (700, 9000, None)])
+def test_deterministic_replayed_and_on_another_stream(new, long, bound):
+    x = Batch([(600, new, 3), (long, new, new // 2), (0, new, 1)], 32, 4 if long < 9000 else 1, 128, seed=6, bound=bound)
     want = x.run()
     x.check(want)
     for _ in range(5):
@@ -216,10 +223,10 @@ def test_deterministic_replayed_and_on_another_stream(new, long):
     assert torch.equal(outs[0], again)
 
 
-@pytest.mark.parametrize("new", [3, 40, 100])
-def test_a_user_does_not_see_its_neighbours_rows(new):
+@pytest.mark.parametrize("new,bound", [(3, None), (40, None), (100, LONG)])
+def test_a_user_does_not_see_its_neighbours_rows(new, bound):
     """q, K and V of one user are NaN: the others' outputs are what they were, bit for bit."""
-    x = Batch([(77, new, 1), (130, new, 2), (40, new, 0)], 16, 2, 64, seed=12)
+    x = Batch([(77, new, 1), (130, new, 2), (40, new, 0)], 16, 2, 64, seed=12, bound=bound)
     want = x.run()
     x.check(want)
     x.q[x.starts[1]:x.starts[2]] = float("nan")
@@ -228,11 +235,11 @@ def test_a_user_does_not_see_its_neighbours_rows(new):
     assert torch.equal(got[:x.starts[1]], want[:x.starts[1]]) and torch.equal(got[x.starts[2]:], want[x.starts[2]:])
 
 
-@pytest.mark.parametrize("new", [3, 40, 100])
-def test_decreasing_offsets(new):
+@pytest.mark.parametrize("new,bound", [(3, None), (40, None), (100, LONG)])
+def test_decreasing_offsets(new, bound):
     """Offsets that step back: reported; the users before the step are computed, nothing else is touched
     beyond the rows the offsets name."""
-    x = Batch([(50, new, 1)] * 4, 16, 2, 64, seed=13)
+    x = Batch([(50, new, 1)] * 4, 16, 2, 64, seed=13, bound=bound)
     off = dev_i32([0, new, 3 * new, 2 * new, 4 * new])
     big = torch.full((4 * new + 8, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
     x.run(off=off, out=big[4:-4])
@@ -241,10 +248,10 @@ def test_decreasing_offsets(new):
     assert torch.all(big[:4] == 5.0) and torch.all(big[-4:] == 5.0)
 
 
-@pytest.mark.parametrize("new", [2, 90])
-def test_shared_prefix_pages(new):
+@pytest.mark.parametrize("new,bound", [(2, None), (90, None), (90, LONG)])
+def test_shared_prefix_pages(new, bound):
     """Two users whose first pages are the same pages."""
-    x = Batch([(64, new, 1), (64, new, 1)], 16, 2, 64, seed=7)
+    x = Batch([(64, new, 1), (64, new, 1)], 16, 2, 64, seed=7, bound=bound)
     p = x.pool
     p.table_h[1, :4] = p.table_h[0, :4]
     table = dev_i32(p.table_h).view(p.table_h.shape)
@@ -252,16 +259,16 @@ def test_shared_prefix_pages(new):
     x.check(x.run(table=table))
 
 
-@pytest.mark.parametrize("new", [3, 50])
-def test_bad_users_and_pages(new):
+@pytest.mark.parametrize("new,bound", [(3, None), (50, None), (50, LONG)])
+def test_bad_users_and_pages(new, bound):
     users = [(50, new, 1)] * 6
-    x = Batch(users, 16, 2, 64, seed=8)
+    x = Batch(users, 16, 2, 64, seed=8, bound=bound)
     kv = x.kv_len.clone()
     kv[1] = new - 1                      # shorter than its new rows
     nt = x.nt.clone()
     nt[2] = new + 1                      # more candidates than new rows
     nt[3] = -1
-    kv[4] = 100000                       # longer than max_kv and its pages
+    kv[4] = 2 * LONG                     # longer than max_kv and its pages
     out = torch.full_like(x.q, 5.0)
     x.run(kv=kv, nt=nt, out=out)
     assert binding.hstu_attn_get_error() == 4
@@ -296,14 +303,14 @@ def test_nothing_to_do():
     assert x.run().shape == (0, 1, 32)
 
 
-@pytest.mark.parametrize("new", [1, 40])
-def test_cache_past_32_bit_offsets(new):
+@pytest.mark.parametrize("new,bound", [(1, None), (40, None), (40, LONG)])
+def test_cache_past_32_bit_offsets(new, bound):
     """Pages whose element offsets do not fit 32 bits: a pool of 2^32 elements' reach, a few pages of it used."""
     H, d, page = 2, 128, 16
     rows = (1 << 32) // (H * d) // page + 40
     k = torch.empty((rows, page, H, d), dtype=torch.bfloat16, device="cuda")
     v = torch.empty_like(k)
-    x = Batch([(70, new, 0)], page, H, d, seed=10)
+    x = Batch([(70, new, 0)], page, H, d, seed=10, bound=bound)
     x.pool.table_h[0, :(70 + new + page - 1) // page] = rows - 1 - 3 * np.arange((70 + new + page - 1) // page)
     x.pool.k, x.pool.v = k, v
     x.pool.put(0, 0, *x.kv[0])
