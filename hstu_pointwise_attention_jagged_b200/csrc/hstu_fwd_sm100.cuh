@@ -326,6 +326,13 @@ __device__ __forceinline__ void silu_tile(uint32_t taddr_s, float half_alpha, in
 // whole ring.)
 __device__ __forceinline__ int group_of_load(int e) { return e < 3 ? e : (e + 3) >> 1; }
 
+// Producers of the paged form that have a copy of a tile to issue.
+template <int D>
+__device__ __forceinline__ int paged_producers(const FwdParams& p) {
+  const int boxes = max(kTileRows >> p.paged.cache.page_shift, 1);
+  return min(kPagedProducers, boxes * FwdCfg<D>::kBlocks);
+}
+
 // Producers of the paged form: kPagedProducers warps, of which `who` = 0 takes the pieces from the queue
 // and does all that the contiguous producer does (see the kernel below), in the same order; the others
 // follow it through the work slots.  They share out the copies: a key tile is one copy for each of its pages
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(kPaged ? kPagedThreads : kNumThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       ptx::mbar_init(bar(ctl->sched_full[s]), 1);
       // MMA, SiLU, epilogue and further producer warps
-      ptx::mbar_init(bar(ctl->sched_empty[s]), 1 + 8 + 4 + (kPaged ? kPagedProducers - 1 : 0));
+      ptx::mbar_init(bar(ctl->sched_empty[s]), 1 + 8 + 4 + (kPaged ? paged_producers<D>(p) - 1 : 0));
     }
     ptx::mbar_init(bar(ctl->drain), 1);
     if constexpr (kPaged) ptx::mbar_init(bar(ctl->v_tail), 1);
@@ -723,7 +730,8 @@ __global__ void __launch_bounds__(kPaged ? kPagedThreads : kNumThreads, 1)
     }
     __syncwarp();
   } else if (kPaged && warp >= kPagedWarp0) {
-    produce_paged<D>(ctl, &tm_q, &tm_k, &tm_v, p, sQ, sKV, lane, warp - kPagedWarp0 + 1);
+    const int who = warp - kPagedWarp0 + 1;
+    if (who < paged_producers<D>(p)) produce_paged<D>(ctl, &tm_q, &tm_k, &tm_v, p, sQ, sKV, lane, who);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer
     // The whole warp runs this loop in step, so the control flow is uniform and the descriptors

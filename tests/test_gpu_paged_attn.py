@@ -298,6 +298,21 @@ def test_bad_users_and_pages(new, bound):
         x.kv[0] = keep
 
 
+@pytest.mark.parametrize("page,d", [(1024, 32), (256, 64), (64, 64), (128, 128), (64, 128), (32, 32)])
+def test_many_short_pieces_with_few_copies_a_tile(page, d):
+    """Few copies a tile leave a producer warp without one; it must not fall behind the others.  Short
+    pieces of many users, repeated: no wait runs out (each would be reported) and nothing changes."""
+    rng = np.random.default_rng(page + d)
+    users = [(int(rng.integers(0, 300)), int(rng.choice([0, 1, 17, 40, 129])), 0) for _ in range(32)]
+    x = Batch(users, page, 6, d, seed=14, bound=LONG)
+    want = x.run()
+    x.check(want)
+    for _ in range(300):
+        got = x.run()
+    assert binding.hstu_attn_get_error() == 0
+    assert torch.equal(got, want)
+
+
 def test_nothing_to_do():
     x = Batch([(5, 0, 0), (0, 0, 0)], 16, 1, 32)
     assert x.run().shape == (0, 1, 32)
