@@ -188,9 +188,9 @@ struct RowsShape {
 
 // Clusters as large as keeps every CTA resident at once and busy with two tiles, if that leaves each CTA a
 // short stretch of tiles: then one launch does it all.  A long stretch takes the equal runs, which ragged
-// lengths cannot unbalance.  (us, d = 128, one row a user: 64 users x 4 heads of 700 rows, 11 tiles a CTA,
-// 18.2 against 24.0; 16 x 4 of 3000, 12 tiles, 20.3 against 24.2; 64 x 4 of ragged histories up to 4096,
-// 64 tiles, 62 against 41; 1 x 4 of 32000, 31 tiles, 29 against 20.)
+// lengths cannot unbalance.  (us, clusters against runs, d = 128, one row a user: 64 users x 4 heads of 700
+// rows, 11 tiles a CTA, 17.6 against 23.4; 16 x 4 of 3000, 12 tiles, 19.9 against 23.1; 64 x 4 of ragged
+// histories up to 4096, 65 tiles, 57 against 40; 1 x 4 of 32000, 32 tiles, 27.7 against 18.8.)
 //
 // More than 16 rows a user come here while the call is short.  Every block of 16 rows reads all keys again,
 // but the tcgen05 kernel has its plan, its fill and tiles of 128 rows to pay for.  (us, here against there:
