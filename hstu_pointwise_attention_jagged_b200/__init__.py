@@ -15,7 +15,8 @@ _BINDING_NAMES = ("HstuError", "hstu_attn_fwd", "hstu_attn_fwd_cached", "hstu_at
                   "hstu_layer_fwd", "hstu_layers_fwd", "plan_contents",
                   "library_path", "load_library")
 
-_PAGED_NAMES = ("hstu_rotary", "hstu_rotary_freqs", "hstu_paged_append", "hstu_paged_attn_fwd")
+_PAGED_NAMES = ("hstu_rotary", "hstu_rotary_freqs", "hstu_paged_append", "hstu_paged_attn_fwd",
+                "hstu_paged_selfcheck_fwd_timeout")
 
 
 def __getattr__(name):

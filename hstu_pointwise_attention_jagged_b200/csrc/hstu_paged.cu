@@ -280,8 +280,8 @@ bool encode_q(CUtensorMap* map, const void* base, int64_t rows, int64_t width, i
 
 // Many rows a user: the plan, then the tcgen05 kernel, over one buffer from the library's pool.
 template <int D>
-hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, float alpha, DeviceState& st,
-                          cudaStream_t stream) {
+hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, float alpha, uint64_t wait_limit_ns,
+                          DeviceState& st, cudaStream_t stream) {
   static std::once_flag once[kMaxDevices];
   static cudaError_t ready[kMaxDevices];
   cudaError_t e = once_per_device(once, ready, [] {
@@ -334,7 +334,7 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   p.half_alpha = 0.5f * alpha;
   p.inv_n = a.inv_n;
   p.err = a.err;
-  p.wait_limit_ns = kWaitLimitNs;
+  p.wait_limit_ns = wait_limit_ns;
   p.paged.cache = a.cache;
   p.paged.plan = s.plan;
   p.paged.partials = reinterpret_cast<float4*>(at + o_partials);
@@ -343,6 +343,61 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
     e = launch_dependent(hstu_fwd_kernel<D, false, true>, ctas, kPagedThreads, FwdCfg<D>::kSmemBytes, 0, stream, tq, tk, tv, p);
   if (cudaFreeAsync(buf, stream) != cudaSuccess && e == cudaSuccess) return HSTU_ERR_CUDA;
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+// hstu_paged_attn_fwd; with limit_ns, its self-check: the tcgen05 kernel with that limit on every wait.
+hstu_status_t run_paged_attn(const void* q, int64_t q_ld, const hstu_paged_cache_t* cache, const int32_t* q_offsets,
+                             const int32_t* kv_len, const int32_t* num_targets, int32_t B, int32_t H, int32_t d,
+                             int32_t total_new, int32_t max_new, int32_t max_kv, float alpha, float N, void* out,
+                             int64_t out_ld, void* stream, uint64_t limit_ns) {
+  if (B < 0 || H < 1 || total_new < 0 || max_new < 0 || max_kv < 0) return HSTU_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(alpha) || !std::isfinite(N) || !(N > 0.0f)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4 || max_kv > INT_MAX - 4096)
+    return HSTU_ERR_UNSUPPORTED;
+  hstu_status_t s = check_cache(cache, d);
+  if (s != HSTU_OK || total_new == 0) return s;
+  if (B == 0) return HSTU_ERR_INVALID_ARGUMENT;  // rows of no user
+  if (!q || !q_offsets || !kv_len || !out) return HSTU_ERR_INVALID_ARGUMENT;
+  const int64_t width = static_cast<int64_t>(H) * d;
+  if ((s = check_ld(q_ld, width)) != HSTU_OK || (s = check_ld(out_ld, width)) != HSTU_OK) return s;
+  if (!aligned16(q) || !aligned16(out)) return HSTU_ERR_UNSUPPORTED;
+  const size_t pool = cache_bytes(*cache, H, d), out_bytes = static_cast<size_t>((total_new - 1) * out_ld + width) * 2;
+  if (overlaps(cache->k, pool, out, out_bytes) || overlaps(cache->v, pool, out, out_bytes) ||
+      rows_overlap(out, out_ld, q, q_ld, total_new, width))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  DeviceState* st = device_state();
+  if (!st) return HSTU_ERR_CUDA;
+  RowsArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_ld = q_ld;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.out_ld = out_ld;
+  a.cache = view_of(*cache);
+  a.q_offsets = q_offsets;
+  a.kv_len = kv_len;
+  a.num_targets = num_targets;
+  a.B = B;
+  a.H = H;
+  a.total_new = total_new;
+  a.max_kv = max_kv;
+  a.half_alpha = 0.5f * alpha;
+  a.inv_n = 1.0f / N;
+  a.err = st->err_word;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int32_t most = max_new < total_new ? max_new : total_new;
+  a.blocks = most > kRowsBlock ? (most + kRowsBlock - 1) / kRowsBlock : 1;
+  a.max_new = most;
+  if (limit_ns || !rows_shape(a, 64 * 128 / d, st->num_sms).few) {
+    const uint64_t limit = limit_ns ? limit_ns : kWaitLimitNs;
+    return d == 128 ? launch_many<128>(a, *cache, alpha, limit, *st, cs)
+                    : (d == 64 ? launch_many<64>(a, *cache, alpha, limit, *st, cs)
+                               : launch_many<32>(a, *cache, alpha, limit, *st, cs));
+  }
+  if (most <= 8)
+    return d == 128 ? launch_rows<128, 8>(a, *st, cs)
+                    : (d == 64 ? launch_rows<64, 8>(a, *st, cs) : launch_rows<32, 8>(a, *st, cs));
+  return d == 128 ? launch_rows<128, 16>(a, *st, cs)
+                  : (d == 64 ? launch_rows<64, 16>(a, *st, cs) : launch_rows<32, 16>(a, *st, cs));
 }
 
 }  // namespace
@@ -435,52 +490,18 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
                                   const int32_t* kv_len, const int32_t* num_targets, int32_t B, int32_t H, int32_t d,
                                   int32_t total_new, int32_t max_new, int32_t max_kv, float alpha, float N, void* out,
                                   int64_t out_ld, void* stream) {
-  using namespace hstu;
-  if (B < 0 || H < 1 || total_new < 0 || max_new < 0 || max_kv < 0) return HSTU_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(alpha) || !std::isfinite(N) || !(N > 0.0f)) return HSTU_ERR_INVALID_ARGUMENT;
-  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4 || max_kv > INT_MAX - 4096)
-    return HSTU_ERR_UNSUPPORTED;
-  hstu_status_t s = check_cache(cache, d);
-  if (s != HSTU_OK || total_new == 0) return s;
-  if (B == 0) return HSTU_ERR_INVALID_ARGUMENT;  // rows of no user
-  if (!q || !q_offsets || !kv_len || !out) return HSTU_ERR_INVALID_ARGUMENT;
-  const int64_t width = static_cast<int64_t>(H) * d;
-  if ((s = check_ld(q_ld, width)) != HSTU_OK || (s = check_ld(out_ld, width)) != HSTU_OK) return s;
-  if (!aligned16(q) || !aligned16(out)) return HSTU_ERR_UNSUPPORTED;
-  const size_t pool = cache_bytes(*cache, H, d), out_bytes = static_cast<size_t>((total_new - 1) * out_ld + width) * 2;
-  if (overlaps(cache->k, pool, out, out_bytes) || overlaps(cache->v, pool, out, out_bytes) ||
-      rows_overlap(out, out_ld, q, q_ld, total_new, width))
-    return HSTU_ERR_INVALID_ARGUMENT;
-  DeviceState* st = device_state();
-  if (!st) return HSTU_ERR_CUDA;
-  RowsArgs a;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_ld = q_ld;
-  a.out = static_cast<__nv_bfloat16*>(out);
-  a.out_ld = out_ld;
-  a.cache = view_of(*cache);
-  a.q_offsets = q_offsets;
-  a.kv_len = kv_len;
-  a.num_targets = num_targets;
-  a.B = B;
-  a.H = H;
-  a.total_new = total_new;
-  a.max_kv = max_kv;
-  a.half_alpha = 0.5f * alpha;
-  a.inv_n = 1.0f / N;
-  a.err = st->err_word;
-  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const int32_t most = max_new < total_new ? max_new : total_new;
-  a.blocks = most > kRowsBlock ? (most + kRowsBlock - 1) / kRowsBlock : 1;
-  a.max_new = most;
-  if (!rows_shape(a, 64 * 128 / d, st->num_sms).few)
-    return d == 128 ? launch_many<128>(a, *cache, alpha, *st, cs)
-                    : (d == 64 ? launch_many<64>(a, *cache, alpha, *st, cs) : launch_many<32>(a, *cache, alpha, *st, cs));
-  if (most <= 8)
-    return d == 128 ? launch_rows<128, 8>(a, *st, cs)
-                    : (d == 64 ? launch_rows<64, 8>(a, *st, cs) : launch_rows<32, 8>(a, *st, cs));
-  return d == 128 ? launch_rows<128, 16>(a, *st, cs)
-                  : (d == 64 ? launch_rows<64, 16>(a, *st, cs) : launch_rows<32, 16>(a, *st, cs));
+  return hstu::run_paged_attn(q, q_ld, cache, q_offsets, kv_len, num_targets, B, H, d, total_new, max_new, max_kv, alpha,
+                              N, out, out_ld, stream, 0);
+}
+
+hstu_status_t hstu_paged_selfcheck_fwd_timeout(const void* q, int64_t q_ld, const hstu_paged_cache_t* cache,
+                                               const int32_t* q_offsets, const int32_t* kv_len,
+                                               const int32_t* num_targets, int32_t B, int32_t H, int32_t d,
+                                               int32_t total_new, int32_t max_new, int32_t max_kv, float alpha, float N,
+                                               void* out, int64_t out_ld, uint64_t limit_ns, void* stream) {
+  if (limit_ns == 0 || limit_ns > 1000000000ull) return HSTU_ERR_INVALID_ARGUMENT;
+  return hstu::run_paged_attn(q, q_ld, cache, q_offsets, kv_len, num_targets, B, H, d, total_new, max_new, max_kv, alpha,
+                              N, out, out_ld, stream, limit_ns);
 }
 
 }  // extern "C"

@@ -27,6 +27,7 @@ namespace {
 decltype(&hstu_rotary) g_rotary = nullptr;
 decltype(&hstu_paged_append) g_append = nullptr;
 decltype(&hstu_paged_attn_fwd) g_attn = nullptr;
+decltype(&hstu_paged_selfcheck_fwd_timeout) g_selfcheck = nullptr;
 PyObject* g_error = nullptr;  // HstuError
 
 // A Python exception is set; unwinds to the function's entry.
@@ -370,12 +371,23 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* k
   });
 }
 
-PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+// hstu_paged_attn_fwd's arguments, then out and stream; with `limit`, limit_ns before those two.
+PyObject* attn(PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames, bool limit) {
   return guarded([&]() -> PyObject* {
     static const char* const names[] = {"q",     "k_cache", "v_cache", "page_table", "q_offsets", "kv_len", "num_targets",
                                         "alpha", "N",       "max_new", "max_kv",     "out",       "stream"};
-    PyObject* a[13];
-    place("hstu_paged_attn_fwd", names, 11, args, nargs, kwnames, a);
+    static const char* const limited[] = {"q", "k_cache", "v_cache", "page_table", "q_offsets", "kv_len", "num_targets",
+                                          "alpha", "N", "max_new", "max_kv", "limit_ns", "out", "stream"};
+    const char* const fn = limit ? "hstu_paged_selfcheck_fwd_timeout" : "hstu_paged_attn_fwd";
+    PyObject *a[13], *b[14];
+    if (limit) {
+      place(fn, limited, 12, args, nargs, kwnames, b);
+      std::memcpy(a, b, 11 * sizeof(a[0]));
+      a[11] = b[12];
+      a[12] = b[13];
+    } else {
+      place(fn, names, 11, args, nargs, kwnames, a);
+    }
     need_library();
     const Rows q = rows_of("q", a[0]);
     const int32_t B = users_of(a[4]);
@@ -385,28 +397,41 @@ PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject*
     const hstu_paged_cache_t cache = cache_of(a[1], a[2], a[3], B, q);
     const float alpha = float_of(a[7]), N = float_of(a[8]);
     const int32_t max_new = int32_of("max_new", a[9]), max_kv = int32_of("max_kv", a[10]);
+    const int32_t limit_ns = limit ? int32_of("limit_ns", b[11]) : 0;
     const Place at(q.device, a[12]);
     Held out;
     const Rows o = output_of("out", a[11], q, at, out.o);
-    check(g_attn(q.p, q.ld, &cache, offsets, lens, targets, B, static_cast<int32_t>(q.H), static_cast<int32_t>(q.d),
-                 static_cast<int32_t>(q.rows), max_new, max_kv, alpha, N, const_cast<void*>(o.p), o.ld,
-                 at.stream.stream()),
-          "hstu_paged_attn_fwd");
+    const int32_t H = static_cast<int32_t>(q.H), d = static_cast<int32_t>(q.d), rows = static_cast<int32_t>(q.rows);
+    check(limit ? g_selfcheck(q.p, q.ld, &cache, offsets, lens, targets, B, H, d, rows, max_new, max_kv, alpha, N,
+                              const_cast<void*>(o.p), o.ld, limit_ns < 0 ? 0u : static_cast<uint64_t>(limit_ns),
+                              at.stream.stream())
+                : g_attn(q.p, q.ld, &cache, offsets, lens, targets, B, H, d, rows, max_new, max_kv, alpha, N,
+                         const_cast<void*>(o.p), o.ld, at.stream.stream()),
+          fn);
     return out.release();
   });
 }
 
-// bind(HstuError, rotary, append, attn_fwd): the error class and the entry points' addresses.
+PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  return attn(args, nargs, kwnames, false);
+}
+
+PyObject* selfcheck(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  return attn(args, nargs, kwnames, true);
+}
+
+// bind(HstuError, rotary, append, attn_fwd, selfcheck): the error class and the entry points' addresses.
 PyObject* bind(PyObject*, PyObject* args) {
   PyObject* error;
-  unsigned long long p[3];
-  if (!PyArg_ParseTuple(args, "OKKK", &error, &p[0], &p[1], &p[2])) return nullptr;
+  unsigned long long p[4];
+  if (!PyArg_ParseTuple(args, "OKKKK", &error, &p[0], &p[1], &p[2], &p[3])) return nullptr;
   Py_INCREF(error);
   Py_XDECREF(g_error);
   g_error = error;
   g_rotary = reinterpret_cast<decltype(g_rotary)>(p[0]);
   g_append = reinterpret_cast<decltype(g_append)>(p[1]);
   g_attn = reinterpret_cast<decltype(g_attn)>(p[2]);
+  g_selfcheck = reinterpret_cast<decltype(g_selfcheck)>(p[3]);
   Py_RETURN_NONE;
 }
 
@@ -430,6 +455,12 @@ PyDoc_STRVAR(kAttnDoc,
              "the paged cache, the new ones included; the last num_targets of them are candidates.  Returns ``out``.\n"
              "See include/hstu_paged.h.");
 
+PyDoc_STRVAR(kSelfcheckDoc,
+             "hstu_paged_selfcheck_fwd_timeout(q, k_cache, v_cache, page_table, q_offsets, kv_len, num_targets, alpha, N, "
+             "max_new, max_kv, limit_ns, out=None, stream=None)\n--\n\n"
+             "hstu_paged_attn_fwd on the kernel for many rows with every wait limited to limit_ns (test hook of the abort\n"
+             "path); returns ``out``, partly written.");
+
 PyMethodDef kMethods[] = {
     {"hstu_rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rotary)), METH_FASTCALL | METH_KEYWORDS,
      kRotaryDoc},
@@ -437,7 +468,9 @@ PyMethodDef kMethods[] = {
      kAppendDoc},
     {"hstu_paged_attn_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attn_fwd)),
      METH_FASTCALL | METH_KEYWORDS, kAttnDoc},
-    {"bind", bind, METH_VARARGS, "bind(error, rotary, append, attn_fwd): the error class and the C entry points."},
+    {"hstu_paged_selfcheck_fwd_timeout", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(selfcheck)),
+     METH_FASTCALL | METH_KEYWORDS, kSelfcheckDoc},
+    {"bind", bind, METH_VARARGS, "bind(error, rotary, append, attn_fwd, selfcheck): the error class and the C entry points."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_paged_native", "Marshalling of the paged calls; see paged.py.", -1, kMethods,

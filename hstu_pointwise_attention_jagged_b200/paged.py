@@ -25,11 +25,13 @@ EXPORTS = (
     "hstu_rotary",
     "hstu_paged_append",
     "hstu_paged_attn_fwd",
+    "hstu_paged_selfcheck_fwd_timeout",
 )
 
 hstu_rotary = _paged_native.hstu_rotary
 hstu_paged_append = _paged_native.hstu_paged_append
 hstu_paged_attn_fwd = _paged_native.hstu_paged_attn_fwd
+hstu_paged_selfcheck_fwd_timeout = _paged_native.hstu_paged_selfcheck_fwd_timeout
 
 _lib = None
 
@@ -44,6 +46,7 @@ def load_library():
         lib.hstu_rotary.argtypes = [vp, i64, vp, i64, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp]
         lib.hstu_paged_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, vp]
         lib.hstu_paged_attn_fwd.argtypes = [vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, i64, vp]
+        lib.hstu_paged_selfcheck_fwd_timeout.argtypes = lib.hstu_paged_attn_fwd.argtypes[:-1] + [ctypes.c_uint64, vp]
         for name in EXPORTS:
             getattr(lib, name).restype = ctypes.c_int
         _paged_native.bind(binding.HstuError, *(ctypes.cast(getattr(lib, name), vp).value for name in EXPORTS))

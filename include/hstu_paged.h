@@ -155,6 +155,19 @@ hstu_status_t hstu_paged_attn_fwd(const void* q, int64_t q_ld, const hstu_paged_
                                   int32_t total_new, int32_t max_new, int32_t max_kv,
                                   float alpha, float N, void* out, int64_t out_ld, void* stream);
 
+/*
+ * hstu_paged_selfcheck_fwd_timeout — hstu_attn_selfcheck_fwd_timeout for the paged kernel: the work of
+ * hstu_paged_attn_fwd on the kernel for many rows, with every pipeline wait limited to limit_ns
+ * nanoseconds (1 .. 1e9).  A wait that runs out is reported as HSTU_ERR_TIMEOUT, the kernel drains what
+ * it started and returns, and the context stays usable; `out` is left partly written.
+ */
+hstu_status_t hstu_paged_selfcheck_fwd_timeout(const void* q, int64_t q_ld, const hstu_paged_cache_t* cache,
+                                               const int32_t* q_offsets, const int32_t* kv_len,
+                                               const int32_t* num_targets, int32_t B, int32_t H, int32_t d,
+                                               int32_t total_new, int32_t max_new, int32_t max_kv,
+                                               float alpha, float N, void* out, int64_t out_ld,
+                                               uint64_t limit_ns, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

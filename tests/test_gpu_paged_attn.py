@@ -298,6 +298,27 @@ def test_bad_users_and_pages(new, bound):
         x.kv[0] = keep
 
 
+@pytest.mark.parametrize("page,d", [(16, 128), (256, 64), (8, 32)])
+def test_abort_path_then_recovers(page, d):
+    """The many-row kernel with every wait limited to 1 us: waits run out in the middle of it, it drains and
+    returns, the device reports the timeout once, and a normal call is right afterwards."""
+    x = Batch([(600, 129, 20), (300, 40, 3), (40, 300, 2)], page, 2, d, seed=15, bound=LONG)
+    p = x.pool
+    assert binding.hstu_attn_get_error() == 0
+    for _ in range(2):
+        paged.hstu_paged_selfcheck_fwd_timeout(x.q, p.k, p.v, p.table, x.off, x.kv_len, x.nt, x.alpha, x.N, x.max_new, x.max_kv,
+                                               1000)
+        assert binding.hstu_attn_get_error() == 5  # HSTU_ERR_TIMEOUT
+        assert binding.hstu_attn_get_error() == 0
+    x.check(x.run())
+    assert binding.hstu_attn_get_error() == 0
+    for bad in (0, 10 ** 9 + 1, -5):
+        with pytest.raises(binding.HstuError) as e:
+            paged.hstu_paged_selfcheck_fwd_timeout(x.q, p.k, p.v, p.table, x.off, x.kv_len, x.nt, x.alpha, x.N, x.max_new,
+                                                   x.max_kv, limit_ns=bad)
+        assert e.value.status == 1
+
+
 @pytest.mark.parametrize("page,d", [(1024, 32), (256, 64), (64, 64), (128, 128), (64, 128), (32, 32)])
 def test_many_short_pieces_with_few_copies_a_tile(page, d):
     """Few copies a tile leave a producer warp without one; it must not fall behind the others.  Short

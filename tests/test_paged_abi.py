@@ -155,3 +155,19 @@ def test_attn_refusals(lib):
         assert _attn(lib, _cache(**kw)) == INVALID, kw
     for kw in (dict(page_size=24), dict(row_stride=129)):
         assert _attn(lib, _cache(**kw)) == UNSUPPORTED, kw
+
+
+def test_selfcheck_limit_refusals(lib):
+    """Limits of 0 and above one second, and hstu_paged_attn_fwd's own refusals with a limit in range."""
+    c = _cache()
+    vp, u64 = ctypes.c_void_p, ctypes.c_uint64
+
+    def call(limit, B=2, rows=8, q=0x10000):
+        return lib.hstu_paged_selfcheck_fwd_timeout(vp(q), 128, ctypes.byref(c), vp(0x20000), vp(0x30000), vp(0), B, 2, 64,
+                                                    rows, 4, 64, 1.0, 1.0, vp(0x40000), 128, u64(limit), vp(0))
+
+    for limit in (0, 10 ** 9 + 1, 2 ** 63):
+        assert call(limit) == INVALID
+    assert call(1000, rows=0) == OK
+    assert call(1000, B=-1) == INVALID
+    assert call(1000, q=0x10002) == UNSUPPORTED
