@@ -21,10 +21,13 @@ namespace {
 
 bool head_size_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
 
+// Extents that no memory has are refused before anything is computed from them.
+constexpr int64_t kMaxElements = 1ll << 46;
+
 // A token tensor's row stride: at least the packed row, a multiple of 16 bytes.
-hstu_status_t check_ld(int64_t ld, int64_t width) {
+hstu_status_t check_ld(int64_t ld, int64_t width, int64_t rows) {
   if (ld < width) return HSTU_ERR_INVALID_ARGUMENT;
-  return (ld % 8) == 0 ? HSTU_OK : HSTU_ERR_UNSUPPORTED;
+  return ld % 8 == 0 && ld <= kMaxElements / rows ? HSTU_OK : HSTU_ERR_UNSUPPORTED;
 }
 
 // Whether two row blocks of `width` elements share an element.  Blocks of one wide matrix (equal
@@ -73,6 +76,7 @@ hstu_status_t check_cache(const hstu_paged_cache_t* c, int32_t d) {
     if (s < d) return HSTU_ERR_INVALID_ARGUMENT;
     if (s % 8 != 0 || s > (1ll << 38)) return HSTU_ERR_UNSUPPORTED;  // tensor-map strides are < 2^40 bytes
   }
+  if (c->page_stride > kMaxElements / c->num_pages) return HSTU_ERR_UNSUPPORTED;
   if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u))
     return HSTU_ERR_UNSUPPORTED;
   return HSTU_OK;
@@ -161,7 +165,7 @@ hstu_status_t launch_rotary(RotArgs& a, int32_t d, bool paged, const DeviceState
   int threads = at_most((a.side_rows * units + 31) / 32 * 32, kRotThreads);
   if (threads < 64) threads = 64;  // the angles and the look-ups: at least one thread a pair, and one a row
   static_assert(kRotMaxPairs <= 64 && kRotMaxRows <= 64, "threads of the smallest block");
-  const int grid = (a.rows + a.block_rows - 1) / a.block_rows;
+  const int64_t grid = (static_cast<int64_t>(a.rows) + a.block_rows - 1) / a.block_rows;
   const int smem = a.block_rows * a.pairs * 8;
   const cudaError_t e = paged ? launch_dependent(rotary_kernel<true>, grid, threads, smem, 0, stream, a)
                               : launch_dependent(rotary_kernel<false>, grid, threads, smem, 0, stream, a);
@@ -359,7 +363,8 @@ hstu_status_t run_paged_attn(const void* q, int64_t q_ld, const hstu_paged_cache
   if (B == 0) return HSTU_ERR_INVALID_ARGUMENT;  // rows of no user
   if (!q || !q_offsets || !kv_len || !out) return HSTU_ERR_INVALID_ARGUMENT;
   const int64_t width = static_cast<int64_t>(H) * d;
-  if ((s = check_ld(q_ld, width)) != HSTU_OK || (s = check_ld(out_ld, width)) != HSTU_OK) return s;
+  for (int64_t ld : {q_ld, out_ld})
+    if ((s = check_ld(ld, width, total_new)) != HSTU_OK) return s;
   if (!aligned16(q) || !aligned16(out)) return HSTU_ERR_UNSUPPORTED;
   const size_t pool = cache_bytes(*cache, H, d), out_bytes = static_cast<size_t>((total_new - 1) * out_ld + width) * 2;
   if (overlaps(cache->k, pool, out, out_bytes) || overlaps(cache->v, pool, out, out_bytes) ||
@@ -417,7 +422,7 @@ hstu_status_t hstu_rotary(const void* q, int64_t q_ld, const void* k, int64_t k_
   const int64_t width = static_cast<int64_t>(H) * d;
   const int64_t lds[4] = {q_ld, q_out_ld, k ? k_ld : width, k ? k_out_ld : width};
   for (int64_t ld : lds)
-    if ((s = check_ld(ld, width)) != HSTU_OK) return s;
+    if ((s = check_ld(ld, width, rows)) != HSTU_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return HSTU_ERR_UNSUPPORTED;
   if (clashes(q_out, q_out_ld, q, q_ld, true, rows, width)) return HSTU_ERR_INVALID_ARGUMENT;
   if (k && (clashes(k_out, k_out_ld, k, k_ld, true, rows, width) ||
@@ -453,7 +458,7 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
   const int64_t width = static_cast<int64_t>(H) * d;
   const int64_t lds[4] = {k_ld, v_ld, q ? q_ld : width, q ? q_out_ld : width};
   for (int64_t ld : lds)
-    if ((s = check_ld(ld, width)) != HSTU_OK) return s;
+    if ((s = check_ld(ld, width, total_new)) != HSTU_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return HSTU_ERR_UNSUPPORTED;
   // The cache overlaps no token tensor; K and V pages may interleave, so only identical ones are refused.
   const size_t pool = cache_bytes(*cache, H, d);

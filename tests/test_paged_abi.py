@@ -171,3 +171,13 @@ def test_selfcheck_limit_refusals(lib):
     assert call(1000, rows=0) == OK
     assert call(1000, B=-1) == INVALID
     assert call(1000, q=0x10002) == UNSUPPORTED
+
+
+def test_extents_beyond_any_memory(lib):
+    """Strides whose extents would not fit 64 bits are refused, not wrapped into small ones."""
+    huge = 1 << 61
+    assert _rotary(lib, q_ld=huge) == UNSUPPORTED and _rotary(lib, qo_ld=huge, rows=1 << 30) == UNSUPPORTED
+    assert _append(lib, k_ld=huge) == UNSUPPORTED and _append(lib, v_ld=huge) == UNSUPPORTED
+    assert _attn(lib, q_ld=huge) == UNSUPPORTED and _attn(lib, out_ld=huge) == UNSUPPORTED
+    for call in (_append, _attn):
+        assert call(lib, _cache(num_pages=1 << 30, page_stride=1 << 34)) == UNSUPPORTED
