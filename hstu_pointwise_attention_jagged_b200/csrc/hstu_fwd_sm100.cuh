@@ -360,7 +360,7 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedView& cache = p.paged.cache;
   const PagedPlan& plan = p.paged.plan;
-  const int M = plan.header[1];
+  const int M = plan.header[1], cut0 = plan.header[2];
   const bool chief = who == 0;
   const int page_rows = 1 << cache.page_shift;
   const int box_rows = page_rows < kTileRows ? page_rows : kTileRows;
@@ -458,7 +458,7 @@ __device__ void produce_paged(Ctl* ctl, const CUtensorMap* tm_q, const CUtensorM
         w.L = y.y;
         w.U = y.z;
         pc = Piece{y.w, z.x, z.y, z.z, z.w};
-        w.kv_start = idx - pc.part * pc.pitch;
+        w.kv_start = idx - cut0 - pc.part * pc.pitch;
       }
       if (!wait_all(bar(ctl->sched_empty[slot]), (sched_par >> slot) & 1u)) {
         ok = false;
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(kPaged ? kPagedThreads : kNumThreads, 1)
           // A piece of a cut item: its sums go to its partial.  The warp that finishes an item's last
           // quarter adds the partials of that quarter in piece order, so the result does not depend on
           // which piece that was.
-          const int first = w.kv_start;  // queue place of part 0
+          const int first = w.kv_start;  // part 0's place among the cut pieces
           const size_t part_quads = (size_t)pc.pitch * (D / 4) * kTileRows;  // between two parts' sums
           float4* sums = p.paged.partials + (size_t)first * (D / 4) * kTileRows + row;
           float4* mine = sums + pc.part * part_quads;

@@ -306,7 +306,7 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   const int64_t max_cut = a.B <= kCachedUsers ? kMaxCutRounds * ctas : 0;
   const size_t o_block = 256, o_done = o_block + pad256((static_cast<size_t>(a.B) + 1) * 4),
                o_pieces = o_done + pad256(4 * max_cut * 4),
-               o_partials = o_pieces + pad256((capacity > max_cut ? capacity : max_cut) * sizeof(PagedPiece)),
+               o_partials = o_pieces + pad256((capacity + max_cut) * sizeof(PagedPiece)),
                bytes = o_partials + static_cast<size_t>(max_cut) * kTileRows * D * 4;
   void* buf = nullptr;
   if (cudaMallocFromPoolAsync(&buf, bytes, st.pool, stream) != cudaSuccess) return HSTU_ERR_CUDA;

@@ -53,7 +53,7 @@ struct PagedPiece {
 static_assert(sizeof(PagedPiece) == 48, "three 16-byte loads");
 
 struct PagedPlan {
-  int32_t* header;       // [4] {pieces taken beyond the CTAs' first ones, pieces, 0, 0}
+  int32_t* header;       // [4] {pieces taken beyond the CTAs' first ones, pieces, whole items before the cut, 0}
   int32_t* block_start;  // [B+1] first block of each user
   int32_t* done;         // [4 * max_cut] finished pieces of a cut item, for each quarter of its rows
   PagedPiece* pieces;    // [max_pieces] the queue
@@ -63,7 +63,7 @@ struct PagedPlan {
 struct PagedFwd {
   PagedView cache;
   PagedPlan plan;
-  float4* partials;  // [queue place][D / 4][128 rows]: fp32 sums of the pieces of cut items
+  float4* partials;  // [place among the cut pieces][D / 4][128 rows]: their fp32 sums
 };
 
 }  // namespace hstu

@@ -4,10 +4,13 @@
 // from a queue by the CTAs.  With many items every piece is a whole item, in waves of users whose
 // K and V fit a quarter of L2, by non-increasing cost within a wave (schedule.cuh).  With few items for the
 // CTAs, whole items can leave SMs idle: 192 items of 26 tiles on 148 SMs take the time of 52 tiles, where
-// 34 would do.  So the plan may cut items into pieces of at most q tiles, choosing q by the
-// estimate rounds * (q + overhead).  The pieces of a cut item leave fp32 partial outputs, and the last one to
-// finish adds them up in order (hstu_fwd_sm100.cuh, epilogue).  Pieces of one key range of one user and head
-// are neighbours in the queue: CTAs that work side by side read the same K and V.
+// 34 would do.  So the plan may cut the items of the first users into pieces of at most q tiles and put them behind
+// the others' whole items, where they fill the last round; it chooses both numbers by an estimate of the
+// time.  The pieces of a cut item leave fp32 partial outputs, and the last one to finish adds them up in order
+// (hstu_fwd_sm100.cuh, epilogue).  Pieces of one key range of one user and head are neighbours in the queue:
+// CTAs that work side by side read the same K and V.  (us, H = 4, d = 128: 16 users x 300 rows of 3300, whole items
+// 60.9, all items in halves 59.2, 4 users' in thirds 54.8; 5 x 1000 of 5000, whole 74.3, all in thirds 70.1, one
+// user's in quarters 63.4; 20 ragged users of up to 300 rows over 1500, all in pieces 30.6, some 24.3.)
 //
 // The plan is one CTA's work between two kernels, so what it costs is latency, much of it fetching
 // instructions that run once: loops are not unrolled, the block scan is one function, 64-bit divisions are
@@ -23,9 +26,12 @@
 namespace hstu {
 
 constexpr int kMaxCutRounds = 4;  // cut items make at most this many pieces for each CTA
+constexpr int kMaxRounds = 4;     // batches of more whole items for each CTA are not cut
 constexpr int kMaxCuts = 16;      // pieces of the longest item
 constexpr int kMinPieceTiles = 2;
-constexpr int kPieceOverhead = 3; // tiles: filling the pipeline, writing and adding the partial (measured)
+// Fitted to measured times, in tiles (1.2 us at d = 128): what a whole item and a piece take beyond their own, and
+// what the last addition takes for each part of an item.  A cut has to promise kCutGain of the time.
+constexpr float kItemOverhead = 1.0f, kPieceOverhead = 2.0f, kPartAdd = 1.2f, kCutGain = 0.08f;
 constexpr int kCachedBlocks = 2048;  // batches up to this many 128-row blocks keep their costs in shared memory
 
 struct PagedSchedArgs {
@@ -74,14 +80,15 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   __shared__ unsigned long long scratch2[kSchedWarps];
   __shared__ int scratch[kSchedWarps];
   __shared__ int first_bad;  // first user whose offsets decrease
-  __shared__ int longest, pieces_of[kMaxCuts + 1];
+  __shared__ int longest, all_tiles;
+  __shared__ int2 s_choice[kSchedWarps];
   __shared__ PagedUser s_user[kCachedUsers];
   __shared__ int s_start[kCachedUsers + 1], s_tiles[kCachedUsers], s_cost[kCachedUsers];
   __shared__ unsigned s_block[kCachedBlocks];  // user | cost << 8
   static_assert(kCachedUsers <= 256, "a user in 8 bits");
   const int tid = threadIdx.x;
   if (tid == 0) {
-    longest = 0;
+    longest = all_tiles = 0;
     first_bad = INT_MAX;
   }
   for (int i = tid; i < kMaxCostBins / 4; i += kSchedThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
@@ -138,18 +145,23 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   auto start_of = [&](int b) { return few_users ? s_start[b] : a.plan.block_start[b]; };
   auto owner = [&](int g) { return few_users ? owner_of(s_start, a.B, g) : owner_of(a.plan.block_start, a.B, g); };
   auto known = [&](int b) { return few_users ? s_user[b] : user(b); };
-  int most_tiles = 0;
+  int most_tiles = 0, sum_tiles = 0;
 #pragma unroll 1
   for (int g = tid; g < nblocks; g += kSchedThreads) {
     const int b = owner(g), cost = block_cost(known(b), g - start_of(b));
     most_tiles = max(most_tiles, cost);
+    sum_tiles += min(cost, 1 << 19);  // only an estimate; kCachedBlocks of them fit
     if (cached) {
       s_block[g] = (unsigned)b | (unsigned)cost << 8;
       atomicMax(&s_cost[b], cost);
     }
   }
   most_tiles = __reduce_max_sync(0xffffffffu, most_tiles);
-  if ((tid & 31) == 0) atomicMax(&longest, most_tiles);
+  sum_tiles = __reduce_add_sync(0xffffffffu, sum_tiles);
+  if ((tid & 31) == 0) {
+    atomicMax(&longest, most_tiles);
+    atomicAdd(&all_tiles, sum_tiles);
+  }
   __syncthreads();
   const int top = longest;
   auto block_of = [&](int g, int& b, int& blk, int& cost) {
@@ -185,64 +197,93 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     to[2] = make_int4(p.tiles, p.parts, p.part, p.pitch);
   };
 
-  // Cuts that can be tried: c pieces of every item may not be more than there is room for.
+  // The cut: the items of the first `cut_users` users in pieces of at most q tiles, behind the whole items of
+  // the others in the queue, or none.
   const int items = nblocks * a.H;
-  const int most = items > 0 ? min(min(kMaxCuts, top / kMinPieceTiles), a.max_cut / items) : 1;
-  if (cached && most > 1) {
-    // Pieces when the longest item is cut in c: kSchedThreads / kMaxCuts threads count the users for each c.
-    {
+  int cut_users = 0, q = 1, cut_places = 0;
+  const int most = items > 0 ? min(kMaxCuts, top / kMinPieceTiles) : 1;
+  if (cached && most > 1 && nblocks <= kMaxRounds * a.num_ctas / a.H) {
+    // Estimated time: rounds of whole items at their mean cost, then rounds of pieces, some of which the CTAs
+    // without an item in the last whole round have taken; no less than the longest item, nor than all of
+    // the work spread evenly.
+    const float mean = (float)all_tiles / nblocks + kItemOverhead, even = mean * items, each = 1.0f / a.num_ctas;
+    auto rounds_of = [&](float n) { return ceilf(n * each - 1e-3f); };
+    auto estimate = [&](int whole, int pieces, float size) {  // size: with the overhead
+      const float rounds = rounds_of((float)whole), idle = rounds * a.num_ctas - whole;
+      const float left = fmaxf((float)pieces - idle * floorf(__fdividef(mean, size)), 0.0f);
+      const float time = rounds * mean + rounds_of(left) * size;
+      return fmaxf(fmaxf(time, whole > 0 ? (float)top : 0.0f), (even + pieces * kPieceOverhead) * each);
+    };
+    float least = estimate(items, 0, 1.0f) * (1.0f - kCutGain);
+    int choice = 0;  // users | c << 16
+    if (even * each + 2.0f * kPartAdd < least) {  // else nothing can reach it
+      // A half warp tries the numbers of users for each q, top / 1 to top / kMaxCuts, in sixteen steps.
       constexpr int kEach = kSchedThreads / kMaxCuts;
       static_assert(kEach == 16, "a half warp each");
-      const int c = tid / kEach + 1;
+      const int c = tid / kEach + 1, lane = tid % kEach, size = cdiv(top, c), step = cdiv(a.B, kEach);
+      const int users = min((lane + 1) * step, a.B);
       int n = 0;
-      if (c <= most) {
-        const int q = cdiv(top, c);
 #pragma unroll 1
-        for (int b = tid % kEach; b < a.B; b += kEach) n += (s_start[b + 1] - s_start[b]) * a.H * cdiv(s_cost[b], q);
-      }
+      for (int b = lane * step; b < users; ++b) n += (s_start[b + 1] - s_start[b]) * a.H * cdiv(s_cost[b], size);
 #pragma unroll
-      for (int o = kEach / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if (tid % kEach == 0) pieces_of[c] = n;
-    }
-    __syncthreads();
-    // The best c by estimated time, ties to the smaller: lane c - 1 of each warp rates c.
-    int best = (tid & 31) + 1, time = INT_MAX;
-    if (best <= most && pieces_of[best] <= a.max_cut)
-      time = cdiv(pieces_of[best], a.num_ctas) * (cdiv(top, best) + (best > 1 ? kPieceOverhead : 0));
-    const int least = __reduce_min_sync(0xffffffffu, time);
-    best = __reduce_min_sync(0xffffffffu, time == least ? best : INT_MAX);
-    if (best > 1) {
-      // Queue places: user, head, part, block.  Every item of a user is cut alike; the places of parts
-      // that a short item does not have stay empty.
-      const int q = cdiv(top, best);
-      const int mine = tid < a.B ? (s_start[tid + 1] - s_start[tid]) * a.H * cdiv(s_cost[tid], q) : 0;
-      int total;
-      const int first = paged_scan(mine, scratch, &total) - mine;
-      if (tid < a.B) s_tiles[tid] = first;
-      __syncthreads();
-#pragma unroll 1
-      for (int x = tid; x < items; x += kSchedThreads) {
-        const int h = x / nblocks;
-        int b, blk, cost;
-        block_of(x - h * nblocks, b, blk, cost);
-        PagedPiece p = piece_of(b, blk, cost);
-        p.h = h;
-        const int parts = cdiv(s_cost[b], q);
-        p.pitch = s_start[b + 1] - s_start[b];
-        p.parts = min(parts, cost);
-        const int at = s_tiles[b] + h * parts * p.pitch + blk;
-#pragma unroll 1
-        for (p.part = 0; p.part < parts; ++p.part) {
-          p.tile0 = p.part < p.parts ? cost * p.part / p.parts : 0;
-          p.tiles = p.part < p.parts ? cost * (p.part + 1) / p.parts - p.tile0 : 0;
-          put(at + p.part * p.pitch, p);
-        }
-        reinterpret_cast<int4*>(a.plan.done)[at] = make_int4(0, 0, 0, 0);
+      for (int o = 1; o < kEach; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, n, o, kEach);
+        if (lane >= o) n += up;
       }
-      if (tid == 0) *reinterpret_cast<int4*>(a.plan.header) = make_int4(0, total, 0, 0);
-      return;
+      if (c > 1 && c <= most && n <= a.max_cut) {
+        const float time = estimate((nblocks - s_start[users]) * a.H, n, size + kPieceOverhead) + c * kPartAdd;
+        if (time < least) {
+          least = time;
+          choice = users | c << 16;
+        }
+      }
+      // The least time of all, ties to the fewest cuts (non-negative floats order like their bits).
+      auto lowest = [&](unsigned time) {
+        const unsigned t = __reduce_min_sync(0xffffffffu, time);
+        choice = (int)__reduce_min_sync(0xffffffffu, time == t ? (unsigned)choice : UINT_MAX);
+        return t;
+      };
+      unsigned t = lowest(__float_as_uint(least));
+      if ((tid & 31) == 0) s_choice[tid >> 5] = make_int2((int)t, choice);
+      __syncthreads();
+      const int2 other = s_choice[min(tid & 31, kSchedWarps - 1)];
+      choice = other.y;
+      lowest((unsigned)other.x);
+    }
+    cut_users = choice & 0xffff;
+    if (cut_users > 0) q = cdiv(top, choice >> 16);
+  }
+  const int cut_blocks = cut_users > 0 ? s_start[cut_users] : 0;  // they are the first ones
+  const int whole = items - cut_blocks * a.H;
+  if (cut_users > 0) {
+    // Queue places: user, head, part, block.  Every item of a user is cut alike; the places of parts
+    // that a short item does not have stay empty.
+    const int mine = tid < cut_users ? (s_start[tid + 1] - s_start[tid]) * a.H * cdiv(s_cost[tid], q) : 0;
+    const int first = paged_scan(mine, scratch, &cut_places) - mine;
+    if (tid < cut_users) s_tiles[tid] = first;
+    __syncthreads();
+#pragma unroll 1
+    for (int x = tid; x < cut_blocks * a.H; x += kSchedThreads) {
+      const int h = x / cut_blocks;
+      int b, blk, cost;
+      block_of(x - h * cut_blocks, b, blk, cost);
+      PagedPiece p = piece_of(b, blk, cost);
+      p.h = h;
+      const int parts = cdiv(s_cost[b], q);
+      p.pitch = s_start[b + 1] - s_start[b];
+      p.parts = min(parts, cost);
+      const int at = s_tiles[b] + h * parts * p.pitch + blk;
+#pragma unroll 1
+      for (p.part = 0; p.part < parts; ++p.part) {
+        p.tile0 = p.part < p.parts ? cost * p.part / p.parts : 0;
+        p.tiles = p.part < p.parts ? cost * (p.part + 1) / p.parts - p.tile0 : 0;
+        put(whole + at + p.part * p.pitch, p);
+      }
+      reinterpret_cast<int4*>(a.plan.done)[at] = make_int4(0, 0, 0, 0);
     }
   }
+  if (tid == 0) *reinterpret_cast<int4*>(a.plan.header) = make_int4(0, whole + cut_places, whole, 0);
+  if (whole == 0) return;
 
   // Whole items: a counting sort of the blocks by (wave, non-increasing cost).  Waves are those the batch
   // reaches, or fewer that hold more; costs are rounded to bins that fit the key space.
@@ -265,12 +306,12 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
     if (key >= 0 && rank == 0) at = atomicAdd(&hist[key], __popc(same) * a.H);
     return __shfl_sync(0xffffffffu, at, leader);
   };
-  const int rounds = cdiv(nblocks, kSchedThreads);
+  const int rounds = cdiv(nblocks - cut_blocks, kSchedThreads);
 #pragma unroll 1
   for (int k = 0; k < rounds; ++k) {
     int b, blk, cost, rank, key = -1;
-    if (k * kSchedThreads + tid < nblocks) {
-      block_of(k * kSchedThreads + tid, b, blk, cost);
+    if (cut_blocks + k * kSchedThreads + tid < nblocks) {
+      block_of(cut_blocks + k * kSchedThreads + tid, b, blk, cost);
       key = key_of(b, cost);
     }
     claim(key, rank);
@@ -294,10 +335,10 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
   __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < rounds; ++k) {
-    const bool there = k * kSchedThreads + tid < nblocks;
+    const bool there = cut_blocks + k * kSchedThreads + tid < nblocks;
     int b, blk, cost, rank, key = -1;
     if (there) {
-      block_of(k * kSchedThreads + tid, b, blk, cost);
+      block_of(cut_blocks + k * kSchedThreads + tid, b, blk, cost);
       key = key_of(b, cost);
     }
     const int at = claim(key, rank);
@@ -306,7 +347,6 @@ __global__ void __launch_bounds__(kSchedThreads) paged_schedule_kernel(const Pag
 #pragma unroll 1
     for (p.h = 0; p.h < a.H; ++p.h) put(at + rank * a.H + p.h, p);
   }
-  if (tid == 0) *reinterpret_cast<int4*>(a.plan.header) = make_int4(0, items, 0, 0);
 }
 
 }  // namespace hstu

@@ -298,6 +298,18 @@ def test_bad_users_and_pages(new, bound):
         x.kv[0] = keep
 
 
+@pytest.mark.parametrize("users", [[(1200, 300, 20)] * 14, [(1200, 300, 0)] * 7 + [(0, 0, 0)] + [(900 + 40 * i, 290, 290) for i in range(8)],
+                                   [(100 * i, 129 + 30 * i, 0) for i in range(1, 13)]], ids=["equal", "two kinds", "ragged"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_whole_items_and_pieces_in_one_plan(users, d):
+    """A little more work than one round of whole items: the plan may cut the first users' items and leave the
+    others whole."""
+    x = Batch(users, 32, 4, d, seed=17, bound=LONG)
+    out = x.run()
+    x.check(out, only={0, 1, 3, len(users) - 1})
+    assert torch.equal(out, x.run())
+
+
 @pytest.mark.parametrize("page,d", [(16, 128), (256, 64), (8, 32)])
 def test_abort_path_then_recovers(page, d):
     """The many-row kernel with every wait limited to 1 us: waits run out in the middle of it, it drains and
