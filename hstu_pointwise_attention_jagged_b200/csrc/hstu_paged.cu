@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "host_state.h"
 #include "hstu_paged.h"
@@ -86,6 +87,48 @@ hstu_status_t check_cache(const hstu_paged_cache_t* c, int32_t d) {
 size_t cache_bytes(const hstu_paged_cache_t& c, int32_t H, int32_t d) {
   return static_cast<size_t>((c.num_pages - 1) * c.page_stride + (c.page_size - 1) * c.row_stride +
                              static_cast<int64_t>(H - 1) * c.head_stride + d) * 2;
+}
+
+// The dimensions of K (and of V) beside the columns, by increasing stride; a dimension of one entry has no stride.
+struct CacheAxes {
+  int64_t n[3], stride[3];
+};
+
+CacheAxes cache_axes(const hstu_paged_cache_t& c, int32_t H) {
+  CacheAxes a = {{c.num_pages, c.page_size, H}, {c.page_stride, c.row_stride, c.head_stride}};
+  for (int i = 0; i < 3; ++i)
+    if (a.n[i] == 1) a.stride[i] = 0;
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (a.stride[j] > a.stride[j + 1]) {
+        std::swap(a.stride[j], a.stride[j + 1]);
+        std::swap(a.n[j], a.n[j + 1]);
+      }
+  return a;
+}
+
+// Whether rows of K can share elements: every stride has to step over all that the smaller ones reach.
+bool rows_share(const CacheAxes& a, int32_t d) {
+  int64_t extent = d;
+  for (int i = 0; i < 3; ++i) {
+    if (a.n[i] == 1) continue;
+    if (a.stride[i] < extent) return true;
+    extent += (a.n[i] - 1) * a.stride[i];
+  }
+  return false;
+}
+
+// Whether two caches of this form, `delta` elements apart, share an element.  With rows that share none, the
+// steps along an axis that bring `delta` within the reach of the smaller strides are the two next to
+// delta / stride.
+bool caches_meet(const CacheAxes& a, int32_t d, int64_t delta, int i = 2) {
+  if (i < 0) return -d < delta && delta < d;
+  if (a.n[i] == 1) return caches_meet(a, d, delta, i - 1);
+  int64_t step = delta / a.stride[i];
+  if (step * a.stride[i] > delta) --step;
+  for (int k = 0; k < 2; ++k, ++step)
+    if (-a.n[i] < step && step < a.n[i] && caches_meet(a, d, delta - step * a.stride[i], i - 1)) return true;
+  return false;
 }
 
 PagedView view_of(const hstu_paged_cache_t& c) {
@@ -460,7 +503,7 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
   for (int64_t ld : lds)
     if ((s = check_ld(ld, width, total_new)) != HSTU_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return HSTU_ERR_UNSUPPORTED;
-  // The cache overlaps no token tensor; K and V pages may interleave, so only identical ones are refused.
+  // The cache overlaps no token tensor, and no element of it is written for two places.
   const size_t pool = cache_bytes(*cache, H, d);
   const void* tokens[4] = {k, v, q, q_out};
   for (int i = 0; i < (q ? 4 : 2); ++i) {
@@ -468,7 +511,10 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
     if (overlaps(cache->k, pool, tokens[i], n) || overlaps(cache->v, pool, tokens[i], n))
       return HSTU_ERR_INVALID_ARGUMENT;
   }
-  if (cache->k == cache->v) return HSTU_ERR_INVALID_ARGUMENT;
+  const CacheAxes axes = cache_axes(*cache, H);
+  if (rows_share(axes, d) ||
+      caches_meet(axes, d, (reinterpret_cast<intptr_t>(cache->v) - reinterpret_cast<intptr_t>(cache->k)) / 2))
+    return HSTU_ERR_INVALID_ARGUMENT;
   if (q && (clashes(q_out, q_out_ld, q, q_ld, true, total_new, width) ||
             clashes(q_out, q_out_ld, k, k_ld, false, total_new, width) ||
             clashes(q_out, q_out_ld, v, v_ld, false, total_new, width)))

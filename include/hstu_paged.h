@@ -109,8 +109,10 @@ hstu_status_t hstu_rotary(const void* q, int64_t q_ld, const void* k, int64_t k_
  * hstu_paged_append — writes every user's new K and V rows to their places in the cache.
  *   q, k, v       device bf16 [total_new, H, d], rows *_ld elements apart.  q may be NULL.
  *   rotation      NULL: K is copied as it is, and q must be NULL.  Otherwise K and q are rotated.
- *   cache         see above; the pages that receive rows must belong to one user only.  No other
- *                 row of the cache is touched.
+ *   cache         see above; the pages that receive rows must belong to one user only, and stand once
+ *                 in its table.  No other row of the cache is touched.  K and V may interleave, but no
+ *                 element may be of both, nor of two rows, heads or pages of one (INVALID_ARGUMENT):
+ *                 of the strides, each is at least the extent of what the smaller ones reach.
  *   q_offsets     device int32 [B+1], q_offsets[0] = 0, non-decreasing, q_offsets[B] = total_new.
  *   kv_len        device int32 [B], kv_len[b] >= n_b: lengths after the call.
  *   q_out         device bf16 [total_new, H, d], the rotated q (may be q itself); NULL with q.
