@@ -325,6 +325,19 @@ bool encode_q(CUtensorMap* map, const void* base, int64_t rows, int64_t width, i
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Pieces the plan may cut items into.  It cuts none in batches of too many users or blocks (each user's last
+// block may be a short one, so there are at least total_new / 128), nor where the longest item is too short; an
+// item becomes at most one piece for each kMinPieceTiles of its tiles, and kMaxCuts.
+int64_t most_cut_pieces(const RowsArgs& a, int64_t items, int ctas) {
+  const int64_t blocks = (static_cast<int64_t>(a.total_new) + kItemRows - 1) / kItemRows;
+  if (a.B > kCachedUsers || blocks > kCachedBlocks || blocks > kMaxRounds * ctas / a.H) return 0;
+  const int longest = cost_bound(a.max_kv) / kMinPieceTiles;
+  const int each = longest < kMaxCuts ? longest : kMaxCuts;
+  if (each < 2) return 0;
+  const int64_t most = static_cast<int64_t>(kMaxCutRounds) * ctas;
+  return items < most / each ? items * each : most;
+}
+
 // Many rows a user: the plan, then the tcgen05 kernel, over one buffer from the library's pool.
 template <int D>
 hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, float alpha, uint64_t wait_limit_ns,
@@ -344,9 +357,8 @@ hstu_status_t launch_many(const RowsArgs& a, const hstu_paged_cache_t& cache, fl
   if (!encode_q(&tq, a.q, a.total_new, width, a.q_ld, D) || !encode_pool(&tk, cache.k, cache, a.H, D) ||
       !encode_pool(&tv, cache.v, cache, a.H, D))
     return HSTU_ERR_CUDA;
-  // header | block_start | done | pieces | partials; items are cut in batches that the plan kernel
-  // keeps on chip, into at most max_cut pieces.
-  const int64_t max_cut = a.B <= kCachedUsers ? kMaxCutRounds * ctas : 0;
+  // header | block_start | done | pieces | partials
+  const int64_t max_cut = most_cut_pieces(a, capacity, ctas);
   const size_t o_block = 256, o_done = o_block + pad256((static_cast<size_t>(a.B) + 1) * 4),
                o_pieces = o_done + pad256(4 * max_cut * 4),
                o_partials = o_pieces + pad256((capacity + max_cut) * sizeof(PagedPiece)),

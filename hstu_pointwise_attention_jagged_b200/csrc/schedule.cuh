@@ -71,10 +71,12 @@ constexpr int kSchedWarps = kSchedThreads / 32;
 constexpr int kMaxCostBins = 4096;
 constexpr int kCachedUsers = 256;  // batches up to this many users keep per-user values in shared memory
 
-// Cost bins a plan needs.  A 128-row item computes at most ceil(L/128) + 1 score tiles; the bins
-// leave twice that room.
+// Score tiles of a 128-row item at most: ceil(L/128) + 1.
+inline int cost_bound(int32_t max_seq_len) { return max_seq_len / kTileRows + 2; }
+
+// Cost bins a plan needs: twice the room that the costs take.
 inline int cost_bins(int32_t max_seq_len) {
-  const int64_t n = 2 * (static_cast<int64_t>(max_seq_len) / kTileRows + 3) + 1;
+  const int64_t n = 2 * (static_cast<int64_t>(cost_bound(max_seq_len)) + 1) + 1;
   return static_cast<int>(n < kMaxCostBins ? n : kMaxCostBins);
 }
 

@@ -144,6 +144,10 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
  *                 shape; a user beyond them is reported as HSTU_ERR_BAD_OFFSETS and skipped).
  *   alpha, N      as in hstu_attn_fwd.
  *   out           device bf16 [total_new, H, d], rows out_ld apart; may overlap neither q nor the cache.
+ * A call that needs a workspace takes it from the library's pool, as in hstu_attn.h (captured into a graph,
+ * the graph owns it): 48 bytes for each head and 128 rows (and each head and user), and where few items may
+ * be cut, 512 * d bytes for each piece they may be cut into, at most 4 for each SM (38 MB at d = 128).  With up
+ * to 16 rows a user: none, or 256 * d bytes for each SM.
  * K, V and q must be finite in the rows that a user owns: a tile's masked pairs get the weight zero, but
  * zero times an infinite V of the same user is not zero.  Nothing else in the cache needs to be:
  * rows behind a user's last one may hold anything.
