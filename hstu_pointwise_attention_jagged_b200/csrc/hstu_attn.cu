@@ -71,8 +71,10 @@ void init_device(DeviceState& st, int dev) {
     e = cudaMemPoolCreate(&st.pool, &props);
   }
   if (e == cudaSuccess) {
-    // Keep up to 64 MiB cached between calls so steady-state calls never reach the driver.
-    uint64_t keep = 64ull << 20;
+    // What a synchronisation leaves cached, so that steady-state calls do not reach the driver: the plans, and
+    // six of the largest workspaces of the paged attention (39 MB) on as many streams.  The backward pass may
+    // take more; that goes back.
+    uint64_t keep = 256ull << 20;
     e = cudaMemPoolSetAttribute(st.pool, cudaMemPoolAttrReleaseThreshold, &keep);
   }
   if (e == cudaSuccess) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&st.err_word), g_error_word);

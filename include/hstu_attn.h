@@ -36,7 +36,8 @@
  * queued on `stream` has completed; the library keeps none of them after it returns.
  * hstu_attn_fwd / hstu_attn_fwd_cached take a small stream-ordered plan buffer (work list,
  * work counter) from the library's own per-device memory pool and return it on the same
- * stream; hstu_attn_plan / hstu_attn_fwd_planned use a plan buffer the caller owns.
+ * stream (the pool keeps up to 256 MiB of what its calls have used, for the next ones);
+ * hstu_attn_plan / hstu_attn_fwd_planned use a plan buffer the caller owns.
  * When total_q (or total_tokens) is 0 nothing is read or written and the token pointers may
  * be NULL.
  *

@@ -84,3 +84,25 @@ def test_workspace_of_few_rows():
     assert Call(8, 300, 3, 2, 64).workspace() == []
     sizes = Call(64, 4000, 1, 4, 128, 40000).workspace()
     assert len(sizes) == 1 and sizes[0] <= 256 * 128 * _sms() + 8 * 64 * 4 + 512
+
+
+def test_pool_keeps_two_concurrent_workspaces():
+    """Two calls in flight on two streams, each with the largest workspace: a synchronisation gives none of their
+    memory back, so the next ones find it there."""
+    calls = [Call(16, 3000, 300, 4, 128) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    free = []
+    for _ in range(3):
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        for call, stream in zip(calls, streams):
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(40_000_000)  # some 20 ms: neither call ends before the other has its memory
+                call.run()
+        during = torch.cuda.mem_get_info()[0]
+        torch.cuda.synchronize()
+        free.append((before, during, torch.cuda.mem_get_info()[0]))
+    # The first round may still grow the pool; from then on it neither shrinks nor grows.
+    assert all(after == during for _, during, after in free), free
+    assert all(during == before for before, during, _ in free[1:]), free
+    assert binding.hstu_attn_get_error() == 0
