@@ -19,6 +19,7 @@
 #include <cstdint>
 #include <cstring>
 #include <optional>
+#include <utility>
 
 #include "hstu_paged.h"
 
@@ -228,6 +229,17 @@ hstu_paged_cache_t cache_of(PyObject* k_cache, PyObject* v_cache, PyObject* page
 // ---------------------------------------------------------------------------------------------
 // Calls
 // ---------------------------------------------------------------------------------------------
+// Runs `f`, which touches no Python object, without the interpreter's lock: an allocation or a launch may have
+// to wait for the driver, and other threads go on meanwhile.
+template <typename F>
+auto unlocked(F&& f) {
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  return f();
+}
+
 // The call's device is current, and `stream` is the one given or the device's current one.
 struct Place {
   std::optional<c10::cuda::CUDAGuard> guard;
@@ -258,8 +270,10 @@ Rows output_of(const char* name, PyObject* o, const Rows& in, const Place& place
   }
   std::optional<c10::cuda::CUDAStreamGuard> guard;
   if (place.own_stream) guard.emplace(place.stream);
-  at::Tensor t = at::detail::empty_cuda({in.rows, in.H, in.d}, at::kBFloat16,
-                                        c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(in.device)), std::nullopt);
+  at::Tensor t = unlocked([&]() -> at::Tensor {
+    return at::detail::empty_cuda({in.rows, in.H, in.d}, at::kBFloat16,
+                                  c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(in.device)), std::nullopt);
+  });
   Rows r = in;
   r.p = address(t);
   r.ld = in.H * in.d;
@@ -329,9 +343,11 @@ PyObject* rotary(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* k
     Held out_q, out_k;
     const Rows qo = output_of("q_out", a[7], q, at, out_q.o);
     if (k.p || given(a[1])) ko = output_of("k_out", a[8], q, at, out_k.o);
-    check(g_rotary(q.p, q.ld, k.p, k.ld, &rot, inverse, static_cast<int32_t>(q.H), static_cast<int32_t>(q.d),
-                   static_cast<int32_t>(q.rows), const_cast<void*>(qo.p), qo.ld, const_cast<void*>(ko.p), ko.ld,
-                   at.stream.stream()),
+    check(unlocked([&] {
+            return g_rotary(q.p, q.ld, k.p, k.ld, &rot, inverse, static_cast<int32_t>(q.H), static_cast<int32_t>(q.d),
+                            static_cast<int32_t>(q.rows), const_cast<void*>(qo.p), qo.ld, const_cast<void*>(ko.p), ko.ld,
+                            at.stream.stream());
+          }),
           "hstu_rotary");
     PyObject* kr = out_k.o ? out_k.o : Py_None;
     return PyTuple_Pack(2, out_q.o, kr);
@@ -362,9 +378,11 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* k
       q = rows_of("q", a[7], &k);
       qo = output_of("q_out", a[12], k, at, out.o);
     }
-    check(g_append(q.p, q.ld, k.p, k.ld, v.p, v.ld, turn ? &rot : nullptr, &cache, offsets, lens, B,
-                   static_cast<int32_t>(k.H), static_cast<int32_t>(k.d), static_cast<int32_t>(k.rows),
-                   const_cast<void*>(qo.p), qo.ld, at.stream.stream()),
+    check(unlocked([&] {
+            return g_append(q.p, q.ld, k.p, k.ld, v.p, v.ld, turn ? &rot : nullptr, &cache, offsets, lens, B,
+                            static_cast<int32_t>(k.H), static_cast<int32_t>(k.d), static_cast<int32_t>(k.rows),
+                            const_cast<void*>(qo.p), qo.ld, at.stream.stream());
+          }),
           "hstu_paged_append");
     if (out.o) return out.release();
     Py_RETURN_NONE;
@@ -402,11 +420,14 @@ PyObject* attn(PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames, bool 
     Held out;
     const Rows o = output_of("out", a[11], q, at, out.o);
     const int32_t H = static_cast<int32_t>(q.H), d = static_cast<int32_t>(q.d), rows = static_cast<int32_t>(q.rows);
-    check(limit ? g_selfcheck(q.p, q.ld, &cache, offsets, lens, targets, B, H, d, rows, max_new, max_kv, alpha, N,
-                              const_cast<void*>(o.p), o.ld, limit_ns < 0 ? 0u : static_cast<uint64_t>(limit_ns),
-                              at.stream.stream())
-                : g_attn(q.p, q.ld, &cache, offsets, lens, targets, B, H, d, rows, max_new, max_kv, alpha, N,
-                         const_cast<void*>(o.p), o.ld, at.stream.stream()),
+    check(unlocked([&] {
+            if (!limit)
+              return g_attn(q.p, q.ld, &cache, offsets, lens, targets, B, H, d, rows, max_new, max_kv, alpha, N,
+                            const_cast<void*>(o.p), o.ld, at.stream.stream());
+            return g_selfcheck(q.p, q.ld, &cache, offsets, lens, targets, B, H, d, rows, max_new, max_kv, alpha, N,
+                               const_cast<void*>(o.p), o.ld, limit_ns < 0 ? 0u : static_cast<uint64_t>(limit_ns),
+                               at.stream.stream());
+          }),
           fn);
     return out.release();
   });
