@@ -37,11 +37,31 @@ def up_to_date() -> bool:
     return _newer(LIB, _inputs())
 
 
+def built_for() -> str:
+    """What the marshalling module's C++ interface is that of: the torch and the Python it is compiled against."""
+    import torch
+    return "torch %s, %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
+def _stamp() -> str:
+    return MODULE + ".built_for"
+
+
+def module_built_for():
+    """built_for() of the build that made the module; None if that is not known."""
+    try:
+        with open(_stamp()) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def build_module(force: bool = False) -> str:
-    """Compiles the marshalling module if a source of it is newer; returns its path."""
+    """Compiles the marshalling module if a source of it is newer, or if it was made for another torch or Python;
+    returns its path."""
     sources = [os.path.join(CSRC, s) for s in MODULE_SOURCES]
-    if not force and _newer(MODULE, sources + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] +
-                            [os.path.abspath(__file__)]):
+    if not force and module_built_for() == built_for() and _newer(
+            MODULE, sources + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]):
         return MODULE
     import torch
     home = os.path.dirname(torch.__file__)
@@ -55,7 +75,11 @@ def build_module(force: bool = False) -> str:
            "-o", tmp] + sources + ["-L" + os.path.join(home, "lib")] + [
            "-l" + lib for lib in ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda")]
     subprocess.run(cmd, check=True)
+    if os.path.exists(_stamp()):
+        os.remove(_stamp())
     os.replace(tmp, MODULE)
+    with open(_stamp(), "w") as f:
+        f.write(built_for())
     return MODULE
 
 

@@ -7,16 +7,22 @@ and in Python its marshalling took ten.  If the library has not been built, impo
 first call raises.
 """
 import ctypes
+import os
 
 import torch
 
-from . import binding
+from . import binding, build
 
+_REBUILD = "(run __graft_entry__.build() or python -m hstu_pointwise_attention_jagged_b200.build)"
+# The module uses torch's C++ interface, which another torch need not have.
+if build.module_built_for() not in (None, build.built_for()):
+    raise RuntimeError("_paged_native.so was built for %s, this is %s %s" % (build.module_built_for(), build.built_for(),
+                                                                             _REBUILD))
 try:
     from . import _paged_native
 except ImportError as e:
-    raise RuntimeError("_paged_native.so is not built (run __graft_entry__.build() or "
-                       "python -m hstu_pointwise_attention_jagged_b200.build)") from e
+    raise RuntimeError("_paged_native.so %s %s" % (
+        "could not be loaded: %s" % e if os.path.exists(build.MODULE) else "is not built", _REBUILD)) from e
 
 MAX_AXES = 4
 
