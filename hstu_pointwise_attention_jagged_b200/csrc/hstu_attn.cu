@@ -24,8 +24,25 @@
 #include "hstu_fwd_sm100.cuh"
 #include "gemm_sm100.cuh"
 #include "schedule.cuh"
+#include "schedule_kernel.cuh"
 
 namespace hstu {
+
+// Self-check of the failure path: one thread waits, through the bounded wait every role of the
+// attention kernel uses, on an mbarrier that nothing ever arrives on.  After limit_ns the wait
+// gives up, records kErrTimeout in the error word and raises the abort flag, and the kernel
+// returns normally: no trap, no hang, and the context stays usable.
+__global__ void wait_timeout_selfcheck_kernel(unsigned* err, uint64_t limit_ns) {
+  __shared__ uint64_t never;
+  __shared__ int32_t abort_flag;
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(ptx::smem_addr(&never), 1);
+    abort_flag = 0;
+    ptx::fence_mbarrier_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) wait_bounded(ptx::smem_addr(&never), 0u, &abort_flag, err, limit_ns);
+}
 
 // Device error word (kErrBadOffsets | kErrTimeout), one per device context.
 __device__ unsigned g_error_word;

@@ -1053,20 +1053,4 @@ __global__ void __launch_bounds__(kPaged ? kPagedThreads : kNumThreads, 1)
   }
 }
 
-// Self-check of the failure path: one thread waits, through the bounded wait every role of the
-// attention kernel uses, on an mbarrier that nothing ever arrives on.  After limit_ns the wait
-// gives up, records kErrTimeout in the error word and raises the abort flag, and the kernel
-// returns normally: no trap, no hang, and the context stays usable.
-static __global__ void wait_timeout_selfcheck_kernel(unsigned* err, uint64_t limit_ns) {
-  __shared__ uint64_t never;
-  __shared__ int32_t abort_flag;
-  if (threadIdx.x == 0) {
-    ptx::mbar_init(ptx::smem_addr(&never), 1);
-    abort_flag = 0;
-    ptx::fence_mbarrier_init();
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) wait_bounded(ptx::smem_addr(&never), 0u, &abort_flag, err, limit_ns);
-}
-
 }  // namespace hstu
