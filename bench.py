@@ -182,7 +182,9 @@ def measured_peak():
         return FALLBACK_PEAK_TFLOPS, "fallback 1.59 PFLOP/s"
 
 
-KERNEL_SOURCES = ("hstu_fwd_sm100.cuh", "schedule.cuh", "sm100_ptx.cuh", "hstu_attn.cu")
+# The attention kernel, the plan that orders its work, what both include, and their launches.
+KERNEL_SOURCES = ("hstu_fwd_sm100.cuh", "paged_cache.cuh", "schedule.cuh", "schedule_kernel.cuh", "sm100_ptx.cuh",
+                  "hstu_attn.cu")
 
 
 def kernel_source_digest():
