@@ -22,8 +22,10 @@ namespace {
 
 bool head_size_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
 
-// Extents that no memory has are refused before anything is computed from them.
+// Extents that no memory has are refused before anything is computed from them, and so are more users than a plan
+// can number with their blocks, or a block's threads step over, in 32 bits.
 constexpr int64_t kMaxElements = 1ll << 46;
+constexpr int32_t kMaxUsers = 1 << 30;
 
 // A token tensor's row stride: at least the packed row, a multiple of 16 bytes.
 hstu_status_t check_ld(int64_t ld, int64_t width, int64_t rows) {
@@ -411,7 +413,7 @@ hstu_status_t run_paged_attn(const void* q, int64_t q_ld, const hstu_paged_cache
                              int64_t out_ld, void* stream, uint64_t limit_ns) {
   if (B < 0 || H < 1 || total_new < 0 || max_new < 0 || max_kv < 0) return HSTU_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(alpha) || !std::isfinite(N) || !(N > 0.0f)) return HSTU_ERR_INVALID_ARGUMENT;
-  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4 || max_kv > INT_MAX - 4096)
+  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4 || max_kv > INT_MAX - 4096 || B > kMaxUsers)
     return HSTU_ERR_UNSUPPORTED;
   hstu_status_t s = check_cache(cache, d);
   if (s != HSTU_OK || total_new == 0) return s;
@@ -503,7 +505,7 @@ hstu_status_t hstu_paged_append(const void* q, int64_t q_ld, const void* k, int6
                                 int32_t total_new, void* q_out, int64_t q_out_ld, void* stream) {
   using namespace hstu;
   if (B < 0 || H < 1 || total_new < 0) return HSTU_ERR_INVALID_ARGUMENT;
-  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4) return HSTU_ERR_UNSUPPORTED;
+  if (!head_size_ok(d) || static_cast<int64_t>(H) * d > INT_MAX / 4 || B > kMaxUsers) return HSTU_ERR_UNSUPPORTED;
   hstu_status_t s = check_cache(cache, d);
   if (s == HSTU_OK && rotation) s = check_rotation(rotation, d, total_new, false);
   if (s != HSTU_OK || total_new == 0) return s;

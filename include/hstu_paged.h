@@ -25,6 +25,7 @@
  * kv_len[b] - n_b + r of its history.  n_b = 0 is legal, and so is a user with no earlier rows.
  * Inconsistent offsets or lengths (see each call) are reported as HSTU_ERR_BAD_OFFSETS and the user is
  * skipped; behind an offset that is smaller than the one before it, other users may be skipped too.
+ * A call takes up to 2^30 users.
  */
 #ifndef HSTU_PAGED_H_
 #define HSTU_PAGED_H_
