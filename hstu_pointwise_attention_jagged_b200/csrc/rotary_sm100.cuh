@@ -98,12 +98,11 @@ __device__ __forceinline__ void turn_unit(RotUnit& u, const float4 (&cs)[4], boo
   u.b = make_uint4(wb[0], wb[1], wb[2], wb[3]);
 }
 
-// freq (radians) as 2^-64 turns, modulo one turn.  The fraction is taken of |freq|, where the difference is
-// exact: a small negative one plus a whole turn would be rounded to 2^-54 turns, 7e-7 radians at a far position.
+// freq (radians) as 2^-64 turns, modulo one turn.  The nearest whole turn is taken off, which is exact for both
+// signs: with the one below, a small negative freq would be rounded to 2^-54 turns, 7e-7 radians at a far position.
 __device__ __forceinline__ uint64_t turns_of(double freq) {
-  const double t = fabs(freq) * 0.15915494309189533577;  // 1 / 2 pi
-  const uint64_t turns = (uint64_t)((t - floor(t)) * 18446744073709551616.0);
-  return freq < 0.0 ? 0 - turns : turns;
+  const double t = freq * 0.15915494309189533577;  // 1 / 2 pi
+  return (uint64_t)__double2ll_rz((t - rint(t)) * 0x1p64);  // half a turn saturates, 2^-64 turns short of it
 }
 
 template <bool kPaged>
