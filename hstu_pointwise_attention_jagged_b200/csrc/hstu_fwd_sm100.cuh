@@ -243,7 +243,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // SiLU + mask + bf16 pack of 32 score columns [32*chunk, 32*chunk+32) of this thread's row,
-// written as 16 packed columns [16*chunk, 16*chunk+16) of the same TMEM row.
+// written as 16 packed columns [16*chunk, 16*chunk+16) of the same TMEM row.  The weights are rounded to bf16 (half
+// a step, 2^-8) because the product with V takes 16-bit operands; its sums stay in fp32 until the output.
 // lim/self are relative to the tile's first key: key column c is visible iff c < lim || c == self.
 // With kRab, a visible pair also gets bias[c] (load_bias: rab_row[min(rel0 - c, rab_max)], its
 // query-key distance clipped to the last table entry; rel0 = query position - first key of the

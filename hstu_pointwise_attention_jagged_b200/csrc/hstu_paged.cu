@@ -244,7 +244,8 @@ struct RowsShape {
 // More than 16 rows a user come here while the call is short.  Every block of 16 rows reads all keys again,
 // but the tcgen05 kernel has its plan, its fill and tiles of 128 rows to pay for.  (us, here against there:
 // 4 users x 4 heads of 100 rows over 1000, d = 128, 13.1 against 18.0; 1 x 4 of 256 over 2000, 13.7 against
-// 24.9; 16 x 4 of 80 over 300, 14.5 against 13.6; 64 x 4 of 24 over 300, 17.6 against 21.0.)
+// 24.9; 16 x 4 of 80 over 300, 14.5 against 13.6; 64 x 4 of 24 over 300, 17.6 against 21.0.)  The limits were set at
+// d = 128; they count tiles of 16 KB, so in keys they grow with 1 / d.
 RowsShape rows_shape(const RowsArgs& a, int keys, int num_sms) {
   const int64_t items = static_cast<int64_t>(a.B) * a.H * a.blocks;
   const int64_t tiles = a.max_kv / keys + 1;  // of an item, at most

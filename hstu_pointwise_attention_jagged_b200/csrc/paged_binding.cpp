@@ -3,7 +3,7 @@
 // Argument marshalling only: every function checks the torch tensors it is given, passes pointers,
 // sizes, strides and the current CUDA stream to the C entry point of the same name, and raises
 // HstuError on a non-zero status.  It does in C++ what binding.py does in Python, because a call for a few
-// rows takes the GPU about three microseconds and the same checks in Python took ten.  The entry
+// rows takes the GPU about three microseconds and the same checks in Python took 13 to 16.  The entry
 // points' addresses come from paged.load_library(), which loads libhstu_attn.so; this module does not link it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -171,7 +171,9 @@ struct RowsCopy {
 template <int D, int R>
 struct RowsMath;
 
-// h = alpha s / 2 -> silu(alpha s) = h + h tanh(h); an invisible pair is selected to zero.
+// h = alpha s / 2 -> silu(alpha s) = h + h tanh(h); an invisible pair is selected to zero.  Its callers round the
+// weight to bf16 (half a step, 2^-8 of it): the product with V takes 16-bit operands, and bf16 keeps the range of
+// scores, as in hstu_fwd_kernel.  The fp32 sums that it goes into are rounded once, at the end.
 __device__ __forceinline__ float rows_silu(float s, float half_alpha, bool visible) {
   const float h = s * half_alpha;
   const float p = fmaf(h, ptx::tanh_approx(h), h);

@@ -10,7 +10,7 @@
 // (hstu_fwd_sm100.cuh, epilogue).  Pieces of one key range of one user and head are neighbours in the queue:
 // CTAs that work side by side read the same K and V.  (us, H = 4, d = 128: 16 users x 300 rows of 3300, whole items
 // 60.9, all items in halves 59.2, 4 users' in thirds 54.8; 5 x 1000 of 5000, whole 74.3, all in thirds 70.1, one
-// user's in quarters 63.4; 20 ragged users of up to 300 rows over 1500, all in pieces 30.6, some 24.3.)
+// user's in quarters 65.2; 20 ragged users of up to 300 rows over 1500, all in pieces 30.6, some 24.3.)
 //
 // The plan is one CTA's work between two kernels, so what it costs is latency, much of it fetching
 // instructions that run once: loops are not unrolled, the block scan is one function, 64-bit divisions are
@@ -30,7 +30,9 @@ constexpr int kMaxRounds = 4;     // batches of more whole items for each CTA ar
 constexpr int kMaxCuts = 16;      // pieces of the longest item
 constexpr int kMinPieceTiles = 2;
 // Fitted to measured times, in tiles (1.2 us at d = 128): what a whole item and a piece take beyond their own, and
-// what the last addition takes for each part of an item.  A cut has to promise kCutGain of the time.
+// what the last addition takes for each part of an item.  A cut has to promise kCutGain of the time.  The same
+// figures serve d = 64 and 32, where a tile takes some 0.85 us and a partial is smaller; one of the shapes compared
+// lost by it (6 ragged users, 8 heads, d = 64: 43.2 -> 45.1 us against cutting all items or none).
 constexpr float kItemOverhead = 1.0f, kPieceOverhead = 2.0f, kPartAdd = 1.2f, kCutGain = 0.08f;
 constexpr int kCachedBlocks = 2048;  // batches up to this many 128-row blocks keep their costs in shared memory
 

@@ -3,7 +3,7 @@
 The functions marshal torch tensors into the C entry points of the same names, as :mod:`.binding`
 does, with the same checks and errors (:class:`~.binding.HstuError` on a non-zero status).  They are
 written in C++ (``csrc/paged_binding.cpp``): a call for a few rows takes the GPU about three microseconds,
-and in Python its marshalling took ten.  If the library has not been built, importing this module or the
+and in Python its marshalling took 13 to 16.  If the library has not been built, importing this module or the
 first call raises.
 """
 import ctypes

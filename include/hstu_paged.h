@@ -13,7 +13,9 @@
  *
  * Status codes, the error word (hstu_attn_get_error), ownership, streams and threads are those of
  * hstu_attn.h.  All tensors are bf16 on the device, 16-byte aligned; products and sums are formed
- * in fp32 and rounded to bf16 once.  The pages that hstu_attn.h cites give neither a cache layout
+ * in fp32, and outputs are rounded to bf16 once.  The attention rounds the weights silu(...) to bf16
+ * as well, for their product with V, and takes their tanh from the hardware's approximation (within
+ * 2^-10.9), as hstu_attn_fwd does.  The pages that hstu_attn.h cites give neither a cache layout
  * nor a rotation: these calls are additions of this library.
  *
  * Row strides.  A token tensor [rows, H, d] has its heads packed (element (t, h, c) at
