@@ -102,7 +102,7 @@ def test_pool_keeps_two_concurrent_workspaces():
         during = torch.cuda.mem_get_info()[0]
         torch.cuda.synchronize()
         free.append((before, during, torch.cuda.mem_get_info()[0]))
-    # The first round may still grow the pool; from then on it neither shrinks nor grows.
+    # The first pair of calls may still grow the pool; from then on it neither shrinks nor grows.
     assert all(after == during for _, during, after in free), free
     assert all(during == before for before, during, _ in free[1:]), free
     assert binding.hstu_attn_get_error() == 0
